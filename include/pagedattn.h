@@ -86,6 +86,11 @@ typedef enum {
 #define PA_DEVERR_QUERY 0x20     /* prefill query_start not ascending, past num_tokens, */
                                  /* or more new tokens than context (or max_query_len)  */
 #define PA_DEVERR_ZERO 0x40      /* int8 zero point outside [-128, 127]                 */
+#define PA_DEVERR_TREE 0x80      /* draft tree: parent not before its child, more than  */
+                                 /* the mask's (or 256) tokens, bad accepted path       */
+#define PA_DEVERR_BLOCKS 0x100   /* device free queue shorter than a step's new blocks  */
+#define PA_DEVERR_QUEUE 0x200    /* device free queue: head or count out of range, or   */
+                                 /* more blocks returned than the ring holds            */
 
 /*
  * partition_size value that lets the library choose the split for a decode call: one
@@ -275,6 +280,193 @@ pa_status copy_blocks(void* k_cache, void* v_cache, float* k_scales, float* v_sc
                       int32_t* k_zeros, int32_t* v_zeros, const int32_t* pairs, int num_pairs,
                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
                       pa_dtype cache_dtype, void* stream);
+
+/* ------------------------------------------------------------------------------------- */
+/* A drafted (speculative) step on the GPU. Several tokens per sequence are drafted ahead  */
+/* as a tree, checked by the model in one step and the longest agreeing path is kept. Each */
+/* step extends the block tables and maps slots (paged_build_step), rotates q and k and    */
+/* writes the cache (rotary_and_cache), attends from the tree (paged_attn_tree), picks the */
+/* accepted path (tree_verify) and moves its K/V behind the context (compact_accepted).    */
+/* Nothing of it needs the host, so a step can be captured in a CUDA graph.                */
+/*                                                                                        */
+/* Trees: sequence s drafts n_s tokens, rows query_start[s] .. query_start[s+1]-1 of the    */
+/* step. parents[row] is the index within the sequence (0 .. n_s-1) of the row's parent,  */
+/* smaller than the row's own index, or -1 for a row right behind the context. Row 0 is   */
+/* the sequence's newest known token, whose K/V is not cached yet; rows behind it are     */
+/* drafts. Row i sees the cached context, its ancestors and itself: bit j % 32 of word     */
+/* j / 32 of its mask is set when it sees row j. At most 256 rows per sequence.           */
+/* ------------------------------------------------------------------------------------- */
+/*
+ * A step's block tables, slot map and positions from request lengths ([KVPaged]
+ * "PagedAttention: OS virtual-memory style management": one block is taken as tokens
+ * accumulate; [KVFail] Key Points: blocks come from a free queue and a step fails when too
+ * few are free). Sequence s holds blocks_held[s] blocks (the first entries of its row of
+ * block_tables) and context_lens[s] cached tokens, and brings new_lens[s] tokens. In
+ * sequence order, each takes max(0, ceil((context + new) / block_size) - held) blocks from
+ * the front of the free queue: the blocks pa_alloc_append_batch would take in the same
+ * state when no block is shared. A partially filled last block must not be shared
+ * (pa_alloc_append copies such a block; this call does not).
+ *   context_lens, new_lens, blocks_held   device int32 [num_seqs]
+ *   parents          device int32 [max_tokens] or NULL (every row the child of the row
+ *                    before it); rows behind the last sequence are not read
+ *   block_tables     device int32 [num_seqs][max_blocks_per_seq]; the new entries are written
+ *   free_blocks      device int32 [free_capacity], a ring of free block ids
+ *   queue_state      device int32 [2]: index of the ring's front, number of free blocks
+ *   total_lens       out, int32 [num_seqs]: context + new
+ *   query_start      out, int32 [num_seqs + 1]: each sequence's first row, then their number
+ *   blocks_held_out, queue_state_out      out, as the inputs, after this step
+ *   slot_mapping     out, int64 [max_tokens]: slot of row i of sequence s, at position
+ *                    context + i; -1 for rows behind the last sequence
+ *   positions        out, int32 [max_tokens] or NULL: context + number of the row's
+ *                    ancestors (context + i without parents); 0 behind the last sequence
+ *   tree_mask        out, uint32 [max_tokens][mask_words] or NULL; 0 behind the last sequence
+ *   mask_words       1 to 8 when tree_mask is given (new_lens at most 32 * mask_words)
+ *   status           out, int32 [1] or NULL: 0, or the PA_DEVERR_* bits that made it fail
+ * All or nothing: a negative length, a table too short or held blocks fewer than the
+ * context needs (PA_DEVERR_CONTEXT), more tokens than max_tokens (PA_DEVERR_QUERY), more
+ * than the mask holds (PA_DEVERR_TREE), a bad queue state (PA_DEVERR_QUEUE) or too few free
+ * blocks (PA_DEVERR_BLOCKS) leave tables, held blocks and queue as they were, and give a
+ * step of no tokens: query_start and masks 0, every slot -1, total_lens = context_lens. A bad
+ * parent is recorded (PA_DEVERR_TREE) and its row treated as one right behind the context;
+ * a row whose block id is outside [0, num_blocks) gets slot -1 (PA_DEVERR_BLOCK_ID).
+ * Every output but block_tables is written in full; none may overlap an input. The same
+ * call on the same inputs gives the same outputs.
+ */
+pa_status paged_build_step(const int32_t* context_lens, const int32_t* new_lens,
+                           const int32_t* blocks_held, const int32_t* parents,
+                           int32_t* block_tables, const int32_t* free_blocks,
+                           const int32_t* queue_state, int num_seqs, int max_blocks_per_seq,
+                           int block_size, int num_blocks, int free_capacity, int max_tokens,
+                           int mask_words, int32_t* total_lens, int32_t* query_start,
+                           int32_t* blocks_held_out, int32_t* queue_state_out,
+                           int64_t* slot_mapping, int32_t* positions, uint32_t* tree_mask,
+                           int32_t* status, void* stream);
+
+/*
+ * Returns blocks to the back of the device free queue: sequence s keeps its first
+ * min(held, ceil(keep_lens[s] / block_size)) blocks, the others go to the queue in sequence
+ * order and, within one, in table order (the order of pa_alloc_free_seq). keep_lens[s] = 0
+ * ends a sequence; its context length returns blocks of drafts that were not accepted.
+ * Blocks of a sequence that shares them must not be returned here. Table entries stay as
+ * they are (blocks_held_out says how many count). Buffers as in paged_build_step;
+ * free_blocks is written. All or nothing: a negative length, held blocks outside [0,
+ * max_blocks_per_seq] (PA_DEVERR_CONTEXT) or a queue that would not hold them
+ * (PA_DEVERR_QUEUE) change nothing.
+ */
+pa_status paged_release_blocks(const int32_t* keep_lens, const int32_t* blocks_held,
+                               const int32_t* block_tables, int32_t* free_blocks,
+                               const int32_t* queue_state, int num_seqs,
+                               int max_blocks_per_seq, int block_size, int free_capacity,
+                               int32_t* blocks_held_out, int32_t* queue_state_out,
+                               int32_t* status, void* stream);
+
+/* Shape, strides and types of one rotary_and_cache call. */
+typedef struct {
+  int num_tokens, num_q_heads, num_kv_heads;
+  int head_dim;             /* 64, 128 or 256                                             */
+  int rotary_dim;           /* leading channels that are rotated: a multiple of 16, at     */
+                            /* most head_dim                                              */
+  int num_axes;             /* 1 to 4 position axes                                       */
+  int sections[4];          /* frequencies of each axis, in order; sum = rotary_dim / 2    */
+  int adjacent_pairs;       /* 0: channel i turns with i + rotary_dim / 2; 1: 2i with 2i+1 */
+  int block_size, num_blocks;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  /* elements from token to token     */
+  pa_dtype in_dtype;        /* q, k, v and q_out: PA_F32 or PA_BF16                        */
+  pa_dtype cache_dtype;
+} pa_rotary_desc;
+
+/*
+ * Rotary positions on q and k, fused with the slot-mapped cache write of k and v. Frequency
+ * i of token t turns the pair (x, y) of its two channels by the angle positions[axis][t] *
+ * inv_freq[i], axis being the one whose section holds i (time, height and width of image and
+ * video tokens; one axis for text):  x' = x cos - y sin, y' = y cos + x sin.
+ * The angle is formed and reduced in float64, so far positions lose nothing; products are
+ * float32. q_out gets the turned q rounded once to in_dtype; the cache gets the turned k and
+ * v, converted as reshape_and_cache does but from float32, with no rounding in between.
+ *   q, k, v, q_out   rows [heads][head_dim], token strides in the descriptor; q_out may be
+ *                    q itself
+ *   positions        int32 [num_axes][num_tokens]
+ *   slot_mapping     int64 [num_tokens]; a negative slot is a padding token: nothing of it
+ *                    is read or written (its q_out row stays as it was)
+ *   inv_freq         float32 [rotary_dim / 2]
+ *   k_scales ..      as in reshape_and_cache
+ * Types as in reshape_and_cache. Tokens must map to distinct slots.
+ */
+pa_status rotary_and_cache(const void* q, const void* k, const void* v, void* q_out,
+                           void* k_cache, void* v_cache, const int32_t* positions,
+                           const int64_t* slot_mapping, const float* inv_freq,
+                           const pa_rotary_desc* desc, const float* k_scales,
+                           const float* v_scales, const int32_t* k_zeros,
+                           const int32_t* v_zeros, void* stream);
+
+/* Bytes of device workspace paged_attn_tree needs (0 for an invalid or empty call). */
+size_t paged_attn_tree_workspace_size(const pa_decode_desc* desc, int num_tokens,
+                                      int max_query_len, int max_context_len);
+
+/*
+ * Attention of a step's drafted tokens over the paged cache. As paged_attn_prefill, except
+ * that row i of sequence s, whose n_s rows are the last n_s of its context_lens[s]
+ * positions, sees every position before context_lens[s] - n_s and, of the rows
+ * themselves, those whose bit is set in its mask (which may be none: a row that sees
+ * nothing at all gets out = 0 and lse = -inf). The masks are taken as they are; they need
+ * not be a tree's.
+ *   tree_mask        uint32 [num_tokens][mask_words], mask_words 1 to 8
+ *   max_query_len    host int >= every n_s, at most 32 * mask_words
+ *   desc             as in paged_attn_decode, partition_size 0 or PA_PARTITION_AUTO (the
+ *                    library splits long contexts and joins the parts)
+ *   workspace        device bytes, >= paged_attn_tree_workspace_size(...), 16-byte aligned;
+ *                    calls that overlap on the GPU need one each
+ * Other arguments and errors as in paged_attn_prefill. bf16 q / out with head_dim 128 and a
+ * group of 1, 2, 4, 8 or 16 run on the tensor cores; other shapes, or
+ * pa_set_decode_impl(1), on the CUDA cores. Rows behind query_start[num_seqs] are neither
+ * read nor written. Results depend on lengths and values, not on where blocks sit.
+ */
+pa_status paged_attn_tree(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int32_t* context_lens,
+                          const int32_t* query_start, const uint32_t* tree_mask,
+                          int mask_words, int num_tokens, int max_query_len, float scale,
+                          void* out, const pa_decode_desc* desc, int max_context_len,
+                          const float* k_scales, const float* v_scales, const int32_t* k_zeros,
+                          const int32_t* v_zeros, float* lse_out, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * The accepted path of each sequence's draft tree under greedy choice: from row 0, whose
+ * token is known, go to the child (lowest index first) whose drafted token is the one the
+ * model chose after its parent, until none agrees or max_accept rows are taken.
+ *   parents, query_start       as above; context_lens int32 [num_seqs], the rows included
+ *   draft_tokens     int64 [num_tokens]: token of each row
+ *   target_tokens    int64 [num_tokens]: the model's choice after each row
+ *   accepted         out, int32 [num_seqs][max_accept]: rows of the path, ascending, then -1
+ *   num_accepted     out, int32 [num_seqs]
+ *   next_tokens      out, int64 [num_seqs]: the model's choice after the last accepted row
+ *   kept_lens        out, int32 [num_seqs]: context without drafts + num_accepted
+ * A sequence without rows gets 0 accepted, next token -1 and kept_lens = context_lens; so does one whose
+ * range is inconsistent (PA_DEVERR_QUERY) or longer than 256 rows (PA_DEVERR_TREE).
+ */
+pa_status tree_verify(const int32_t* parents, const int64_t* draft_tokens,
+                      const int64_t* target_tokens, const int32_t* query_start,
+                      const int32_t* context_lens, int num_seqs, int num_tokens,
+                      int max_accept, int32_t* accepted, int32_t* num_accepted,
+                      int64_t* next_tokens, int32_t* kept_lens, void* stream);
+
+/*
+ * Moves the K/V of accepted rows behind the context, in place: for i < num_accepted[s],
+ * position context_lens[s] - n_s + accepted[s][i] is copied to position context_lens[s] -
+ * n_s + i, K and V of every kv head. Codes of fp8 / int8 caches move as they are between
+ * blocks with equal scales (and zero points); otherwise their value is converted again
+ * with the destination's, as reshape_and_cache would. Positions behind the path keep what
+ * they held. The positions written must lie in blocks that no other sequence shares. A path
+ * that is not strictly ascending within the sequence's rows moves nothing (PA_DEVERR_TREE).
+ * accepted: int32 [num_seqs][max_accept], max_accept at most 256.
+ */
+pa_status compact_accepted(void* k_cache, void* v_cache, const int32_t* block_tables,
+                           const int32_t* context_lens, const int32_t* query_start,
+                           const int32_t* accepted, const int32_t* num_accepted, int num_seqs,
+                           int max_accept, int max_blocks_per_seq, int num_kv_heads,
+                           int head_dim, int block_size, int num_blocks, pa_dtype cache_dtype,
+                           const float* k_scales, const float* v_scales,
+                           const int32_t* k_zeros, const int32_t* v_zeros, void* stream);
 
 /*
  * Reads and clears the device error word of the current device (a bitwise OR of

@@ -35,6 +35,7 @@ PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_PAIR, PA_DEVERR_CONTEXT, PA_DEVERR
     0x1, 0x2, 0x4, 0x8, 0x10
 PA_DEVERR_QUERY = 0x20
 PA_DEVERR_ZERO = 0x40
+PA_DEVERR_TREE, PA_DEVERR_BLOCKS, PA_DEVERR_QUEUE = 0x80, 0x100, 0x200
 _STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID", -2: "PA_ERR_UNSUPPORTED", -3: "PA_ERR_CUDA",
            -4: "PA_ERR_NO_BLOCKS", -5: "PA_ERR_WORKSPACE", -6: "PA_ERR_DEVICE"}
 
@@ -56,6 +57,17 @@ class pa_decode_desc(ctypes.Structure):
                 ("num_blocks", ctypes.c_int), ("partition_size", ctypes.c_int),
                 ("q_dtype", ctypes.c_int), ("kv_dtype", ctypes.c_int),
                 ("out_dtype", ctypes.c_int)]
+
+
+class pa_rotary_desc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int), ("num_q_heads", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("num_axes", ctypes.c_int),
+                ("sections", ctypes.c_int * 4), ("adjacent_pairs", ctypes.c_int),
+                ("block_size", ctypes.c_int), ("num_blocks", ctypes.c_int),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int), ("cache_dtype", ctypes.c_int)]
 
 
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -94,6 +106,14 @@ _SIGS = {
     "pa_alloc_cache_stats": (_i, [_vp, _P(_i64), _P(_i64)]),
     "pa_alloc_block_hash": (_i, [_vp, _i, _vp]),
     "pa_sha256": (None, [_vp, _sz, _vp]),
+    "paged_build_step": (_i, [_vp] * 7 + [_i] * 7 + [_vp] * 9),
+    "paged_release_blocks": (_i, [_vp] * 5 + [_i] * 4 + [_vp] * 4),
+    "rotary_and_cache": (_i, [_vp] * 9 + [_P(pa_rotary_desc)] + [_vp] * 5),
+    "paged_attn_tree_workspace_size": (_sz, [_P(pa_decode_desc), _i, _i, _i]),
+    "paged_attn_tree": (_i, [_vp] * 7 + [_i, _i, _i, _f, _vp, _P(pa_decode_desc), _i] + [_vp] * 6 +
+                        [_sz, _vp]),
+    "tree_verify": (_i, [_vp] * 5 + [_i] * 3 + [_vp] * 5),
+    "compact_accepted": (_i, [_vp] * 7 + [_i] * 8 + [_vp] * 5),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -490,3 +510,7 @@ class BlockAllocator:
             if n < 0 or n > max_blocks:
                 raise PagedAttnError(PA_ERR_INVALID, "block table wider than max_blocks")
         return out
+
+
+from .drafted import (build_step, compact_accepted, paged_attn_tree, release_blocks,  # noqa: E402
+                      rotary_and_cache, tree_verify, tree_workspace_size)

@@ -2,8 +2,8 @@
 
     python paged_kv_cache_465_b200/build.py [-v]
 
-The CUDA sources are compiled as one translation unit (pagedattn.cu includes the kernel
-headers), the host allocator separately; the CUDA runtime is linked statically so the
+The CUDA sources are compiled as one translation unit (library.cu includes pagedattn.cu and
+the kernel headers), the host allocator separately; the CUDA runtime is linked statically so the
 library has no dependency on the process's libcudart.
 """
 from __future__ import annotations
@@ -52,7 +52,7 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     cpp_obj = os.path.join(BUILD, "allocator.o")
     cmds = [
         [nvcc, *ARCH, "-lineinfo", *common, "-Xptxas", "-v" if verbose else "-O3",
-         "-c", os.path.join(CSRC, "pagedattn.cu"), "-o", cu_obj] + list(extra or []),
+         "-c", os.path.join(CSRC, "library.cu"), "-o", cu_obj] + list(extra or []),
         [nvcc, *common, "-Wno-deprecated-gpu-targets", "-x", "c++", "-c", os.path.join(CSRC, "allocator.cpp"), "-o", cpp_obj],
         [nvcc, *ARCH, "-shared", "-cudart", "static", cu_obj, cpp_obj, "-o", LIB + ".tmp"],
     ]

@@ -11,8 +11,9 @@ from typing import Iterable, List, Optional, Sequence, Tuple
 
 import numpy as np
 
-from . import (BlockAllocator, copy_blocks, paged_attn_decode, paged_attn_prefill,
-               reshape_and_cache, workspace_size, decode_desc_for)
+from . import (BlockAllocator, compact_accepted, copy_blocks, paged_attn_decode,
+               paged_attn_prefill, paged_attn_tree, reshape_and_cache, rotary_and_cache,
+               tree_workspace_size, workspace_size, decode_desc_for)
 
 _TORCH_DTYPE = {"f32": "float32", "bf16": "bfloat16", "fp8": "uint8", "int8": "int8"}
 
@@ -61,6 +62,16 @@ class PagedKVCache:
     def block_tables(self, seqs: Sequence[int], max_blocks: int):
         return self.torch.from_numpy(self.alloc.padded_tables(seqs, max_blocks))
 
+    def free_ring(self):
+        """The free queue as ``build_step`` and ``release_blocks`` take it, on the device:
+        (ring of num_blocks entries, [front index, count]). From here on the queue is the
+        GPU's: the host allocator does not see what is taken from it."""
+        order = self.alloc.free_queue()
+        ring = self.torch.full((self.num_blocks,), -1, dtype=self.torch.int32)
+        ring[:len(order)] = self.torch.tensor(order, dtype=self.torch.int32)
+        dev = self.k_cache.device
+        return ring.to(dev), self.torch.tensor([0, len(order)], dtype=self.torch.int32, device=dev)
+
     # ---- device operations -------------------------------------------------------------
     def write(self, k, v, slots, stream=None) -> None:
         reshape_and_cache(k, v, self.k_cache, self.v_cache, slots, k_scales=self.k_scales,
@@ -93,3 +104,31 @@ class PagedKVCache:
                                   max_context_len=max_context_len, k_scales=self.k_scales,
                                   v_scales=self.v_scales, k_zeros=self.k_zeros,
                                   v_zeros=self.v_zeros, lse_out=lse_out, stream=stream)
+
+    # ---- a drafted step (build_step, release_blocks and tree_verify need no pool) ----------
+    def rotary_write(self, q, k, v, q_out, positions, slots, inv_freq, *, sections=None,
+                     adjacent_pairs: bool = False, stream=None) -> None:
+        rotary_and_cache(q, k, v, q_out, self.k_cache, self.v_cache, positions, slots, inv_freq,
+                         sections=sections, adjacent_pairs=adjacent_pairs,
+                         k_scales=self.k_scales, v_scales=self.v_scales, k_zeros=self.k_zeros,
+                         v_zeros=self.v_zeros, stream=stream)
+
+    def tree_workspace_bytes(self, q, block_tables, *, max_query_len: int,
+                             max_context_len: int) -> int:
+        return tree_workspace_size(q, self.k_cache, block_tables, max_query_len=max_query_len,
+                                   max_context_len=max_context_len)
+
+    def tree(self, q, block_tables, context_lens, query_start, tree_mask, scale: float, out, *,
+             max_query_len: int, max_context_len: int, lse_out=None, workspace=None, stream=None):
+        return paged_attn_tree(q, self.k_cache, self.v_cache, block_tables, context_lens,
+                               query_start, tree_mask, scale, out, max_query_len=max_query_len,
+                               max_context_len=max_context_len, k_scales=self.k_scales,
+                               v_scales=self.v_scales, k_zeros=self.k_zeros,
+                               v_zeros=self.v_zeros, lse_out=lse_out, workspace=workspace,
+                               stream=stream)
+
+    def compact(self, block_tables, context_lens, query_start, accepted, num_accepted,
+                stream=None) -> None:
+        compact_accepted(self.k_cache, self.v_cache, block_tables, context_lens, query_start,
+                         accepted, num_accepted, k_scales=self.k_scales, v_scales=self.v_scales,
+                         k_zeros=self.k_zeros, v_zeros=self.v_zeros, stream=stream)
