@@ -306,17 +306,21 @@ def _own_tree(s):
 def _own_build(s):
     import paged_kv_cache_465_b200 as pa
     c = s["case"]
-    pa.release_blocks(s["keep"], s["held"], s["block_tables"], s["ring"], s["queue"],
-                      block_size=c["bs"], blocks_held_out=s["held_mid"],
-                      queue_state_out=s["queue_mid"], status=s["status"][:1])
-    pa.build_step(s["context"], s["new"], s["held_mid"], s["block_tables"], s["ring"],
-                  s["queue_mid"], block_size=c["bs"], num_blocks=s["num_blocks"],
-                  total_lens=s["total_lens"], query_start=s["query_start"],
-                  blocks_held_out=s["held_out"], queue_state_out=s["queue_out"],
-                  slot_mapping=s["slots"], positions=s["positions"], parents=s["parents"],
+    # the tables are extended in place: every pass starts from those of the state
+    if "tables" not in s:
+        s["tables"] = torch.empty_like(s["block_tables"])
+    bt = s["tables"].copy_(s["block_tables"])
+    pa.release_blocks(s["keep"], s["held"], bt, s["ring"], s["queue"], block_size=c["bs"],
+                      blocks_held_out=s["held_mid"], queue_state_out=s["queue_mid"],
+                      status=s["status"][:1])
+    pa.build_step(s["context"], s["new"], s["held_mid"], bt, s["ring"], s["queue_mid"],
+                  block_size=c["bs"], num_blocks=s["num_blocks"], total_lens=s["total_lens"],
+                  query_start=s["query_start"], blocks_held_out=s["held_out"],
+                  queue_state_out=s["queue_out"], slot_mapping=s["slots"],
+                  positions=s["positions"], parents=s["parents"],
                   tree_mask=s["mask"] if c["tree"] else None, status=s["status"][1:])
-    return [s[n] for n in ("block_tables", "ring", "held_out", "queue_out", "total_lens",
-                           "query_start", "slots", "positions", "mask", "status")]
+    return [bt] + [s[n] for n in ("ring", "held_out", "queue_out", "total_lens", "query_start",
+                                  "slots", "positions", "mask", "status")]
 
 
 def _own_rotary(s):
