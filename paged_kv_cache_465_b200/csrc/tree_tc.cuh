@@ -1,0 +1,1030 @@
+// Attention of drafted tokens over the paged cache on the fifth-generation tensor cores.
+//
+// Mathematics: for a tile of 128 rows, a row being a (drafted token, query head of the kv
+// head's group) pair, S = Q K^T over 64 keys at a time, a running maximum m and sum l per row
+// (log2 domain), O = sum 2^(S - m) V; a row sees every key before the drafts and, of the
+// drafts, those in its mask. Parts of one context join as
+//   M = max m_p,  out = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p.
+//
+// Bound: HBM while a sequence drafts at most one row tile (a key's K and V cross HBM once for
+// all its rows), tensor and exponential units beyond.
+//
+// Work split: the batch is laid out as one line of key tiles (row tile by row tile, sequence
+// by sequence, kv head by kv head) and cut into equal runs, one per CTA, two CTAs per SM, all
+// resident. Every CTA streams its run without a pause from one (sequence, kv head) to the
+// next, so neither ragged lengths nor few long contexts leave an SM idle, and at most two
+// pieces of a run (its ends) are partial: those go to a workspace whose size does not depend
+// on the contexts, and a second, small launch joins them. Each CTA finds its run by summing
+// the sequences' tiles itself; there is no plan kernel and no counter to reset. Cuts fall by
+// lengths only, so results do not depend on where blocks sit.
+//
+//   warp 5       TMA: Q of the run's current row tile; K and V tiles through their rings, one
+//                (block, 64-channel half) box per lane; block ids and scales read a window of
+//                32 blocks ahead;
+//   warp 4       tcgen05.mma, one lane: S(g + 1) = Q K^T into one of two buffers in tensor
+//                memory while S(g) is in softmax, then O += P(g) V, P read from tensor memory;
+//   warps 0-3    softmax, one thread per row (= tensor-memory lane): mask, running maximum
+//                with lazy rescaling, P as bf16 pairs over S; O / l or the partial at the end;
+//   warps 6, 7   fp8 / int8 caches: turn the codes that TMA staged into the bf16 tiles the
+//                products read (exact values; scales go to the scores and to P).
+// Two CTAs per SM hide each other's starts, ends and waits.
+//
+// Every wait is bounded; a CTA that gives up flags PA_DEVERR_TIMEOUT, lets its copies and
+// products finish and releases its tensor memory.
+#pragma once
+
+#include "prefill_tc.cuh"
+#include "tree_simt.cuh"
+
+namespace pa {
+namespace tree {
+
+using pf::sdesc;
+using pf::tc_fence_after;
+using pf::tc_fence_before;
+using pf::tmem_ld32;
+using pf::tmem_st32;
+using pf::tmem_wait_ld;
+using pf::tmem_wait_st;
+using pf::umma_commit;
+using tc::mbar_arrive;
+using tc::mbar_arrive_tx;
+using tc::mbar_init;
+using tc::mbar_wait;
+using tc::smem_u32;
+
+constexpr int kRows = 128;                 // rows of a tile
+constexpr int kKeys = 64;                  // keys of a tile
+constexpr int kDim = 128;
+constexpr int kStreams = 296;              // runs the batch is cut into: two CTAs per SM of 148
+constexpr int kMmaWarp = 4, kTmaWarp = 5, kConvWarp = 6;
+constexpr int kQSlab = kRows * 128;        // 64 channels (128 B) x 128 rows
+constexpr int kQBytes = 2 * kQSlab;
+constexpr int kKVSlab = kKeys * 128;       // 64 channels x 64 keys
+constexpr int kKVBytes = 2 * kKVSlab;
+constexpr int kCodeBytes = kKeys * 128;    // one-byte codes of 64 keys
+constexpr int kMaxTileBlocks = kKeys / 8;  // blocks of a key tile, at most
+constexpr int kInfo = 8;                   // ring of per-tile facts for softmax and converters
+constexpr uint32_t kCols = 256;            // tensor memory: S at 0 and 64 (P over it), O at 128
+constexpr uint32_t kOCol = 128;
+
+// What the producer knows about a key tile.
+struct TileInfo {
+  uint32_t bad;                            // bit b: block b of the tile cannot be read
+  float ks[kMaxTileBlocks], vs[kMaxTileBlocks];
+  int kz[kMaxTileBlocks], vz[kMaxTileBlocks];
+};
+
+template <bool QUANT>
+struct Layout {
+  static constexpr int kThreads = QUANT ? 256 : 192;
+  static constexpr int kKSt = QUANT ? 1 : 2;     // bf16 tiles of K and of V
+  static constexpr int kVSt = QUANT ? 1 : 2;
+  static constexpr int kK8St = QUANT ? 3 : 0;    // staged codes
+  static constexpr int kV8St = QUANT ? 2 : 0;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kQBytes;
+  static constexpr int kOffV = kOffK + kKSt * kKVBytes;
+  static constexpr int kOffK8 = kOffV + kVSt * kKVBytes;
+  static constexpr int kOffV8 = kOffK8 + kK8St * kCodeBytes;
+  static constexpr int kOffInfo = kOffV8 + kV8St * kCodeBytes;
+  static constexpr int kOffMisc = kOffInfo + kInfo * (int)sizeof(TileInfo);
+  static constexpr int kOffBar = kOffMisc + 384;
+  // barriers
+  static constexpr int kBarQF = 0, kBarQE = 1;
+  static constexpr int kBarKF = 2, kBarKE = kBarKF + kKSt;
+  static constexpr int kBarVF = kBarKE + kKSt, kBarVE = kBarVF + kVSt;
+  static constexpr int kBarSF = kBarVE + kVSt;   // [2] S in tensor memory
+  static constexpr int kBarP = kBarSF + 2;       // [2] P in tensor memory
+  static constexpr int kBarO = kBarP + 2;        // [2] P V done
+  static constexpr int kBarInfo = kBarO + 2;     // [kInfo]
+  static constexpr int kBarK8F = kBarInfo + kInfo, kBarK8E = kBarK8F + kK8St;
+  static constexpr int kBarV8F = kBarK8E + kK8St, kBarV8E = kBarV8F + kV8St;
+  static constexpr int kBarSm = kBarV8E + kV8St;  // the four softmax warps, once a piece
+  static constexpr int kBarFin = kBarSm + 1;
+  static constexpr int kNumBars = kBarFin + 1;
+  static constexpr int kSmem = kOffBar + 8 * kNumBars + 1024;  // + alignment slack
+};
+static_assert(Layout<true>::kSmem <= 113 * 1024 && Layout<false>::kSmem <= 113 * 1024,
+              "two CTAs per SM");
+static_assert(kInfo * sizeof(TileInfo) % 8 == 0, "barriers are 8-byte aligned");
+
+// S = Q K^T: A and B K-major, N = 64 keys. O += P V: A from tensor memory, B MN-major, N = 128.
+constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kKeys >> 3) << 17) |
+                             ((uint32_t)(kRows >> 4) << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
+                              ((uint32_t)(kDim >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+
+// Workspace: what CTA b's run is, then the partial pieces.
+struct RunInfo {
+  int64_t per;       // key tiles of a run
+  int64_t begin;     // first tile of the (row tile, sequence, kv head) that the run begins in
+  int rt, s, kvh, tiles;  // that one, and its key tiles; tiles = 0: the run is empty
+};
+struct Workspace {
+  RunInfo* runs;     // [kStreams]
+  float* m;          // [kStreams][2][kRows]: piece 0 begins the run, piece 1 ends it
+  float* l;
+  float* acc;        // [kStreams][2][kDim / 4][kRows][4]
+};
+constexpr size_t kRunBytes = (size_t)kStreams * sizeof(RunInfo);
+constexpr size_t kPieceRows = (size_t)kStreams * 2 * kRows;
+constexpr size_t kWorkspaceBytes =
+    (kRunBytes + 255) / 256 * 256 + kPieceRows * (2 + kDim) * sizeof(float);
+inline Workspace workspace_at(void* p) {
+  Workspace w;
+  char* c = static_cast<char*>(p);
+  w.runs = reinterpret_cast<RunInfo*>(c);
+  w.m = reinterpret_cast<float*>(c + (kRunBytes + 255) / 256 * 256);
+  w.l = w.m + kPieceRows;
+  w.acc = w.l + kPieceRows;
+  return w;
+}
+
+// A piece of a run: key tiles [t0, t1) of row tile rt, sequence s, kv head kvh.
+struct Piece {
+  int rt, s, kvh, t0, t1, tiles;
+  int q0, n, ctx;
+};
+
+__device__ __forceinline__ int tiles_of(int ctx) { return (ctx + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int row_tiles_of(int n, int G) {
+  return (int)(((int64_t)n * G + kRows - 1) / kRows);
+}
+
+// The pieces of a run in order, the same for every warp that walks it: 32 sequences' ranges
+// are held one per lane. All members but those are warp-uniform; every lane takes part.
+struct Walk {
+  int64_t left;
+  int rt, s, kvh, tile, tiles, base;
+  int l_q0, l_n, l_ctx;  // this lane's sequence base + lane (n = 0: none, or nothing to do)
+
+  __device__ __forceinline__ void load(const TreeArgs& a) {
+    const int k = base + (threadIdx.x & 31);
+    l_n = 0;
+    if (k < a.num_seqs && !seq_range(a, k, l_q0, l_n, l_ctx)) l_n = 0;
+  }
+  __device__ __forceinline__ void start(const TreeArgs& a, int64_t count, int rt_, int s_, int kvh_,
+                                        int tile_) {
+    left = count;
+    rt = rt_;
+    s = s_;
+    kvh = kvh_;
+    tile = tile_;
+    base = s & ~31;
+    if (left > 0) {
+      load(a);
+      tiles = tiles_of(__shfl_sync(0xffffffffu, l_ctx, s & 31));
+    }
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a, Piece& p) {
+    if (left <= 0) return false;
+    if (tile == tiles) {
+      tile = 0;
+      if (++kvh == a.num_kv_heads) {
+        kvh = 0;
+        int from = (s & 31) + 1;
+        while (true) {
+          const unsigned v = __ballot_sync(
+              0xffffffffu, (int)(threadIdx.x & 31) >= from && (int64_t)l_n * a.group > (int64_t)rt * kRows);
+          if (v) {
+            s = base + __ffs(v) - 1;
+            break;
+          }
+          from = 0;
+          base += 32;
+          if (base >= a.num_seqs) {
+            base = 0;
+            if ((int64_t)++rt * kRows >= (int64_t)a.max_query_len * a.group) {
+              left = 0;  // cannot happen while `left` counts tiles that exist
+              return false;
+            }
+          }
+          load(a);
+        }
+        tiles = tiles_of(__shfl_sync(0xffffffffu, l_ctx, s & 31));
+      }
+    }
+    p.rt = rt;
+    p.s = s;
+    p.kvh = kvh;
+    p.tiles = tiles;
+    p.q0 = __shfl_sync(0xffffffffu, l_q0, s & 31);
+    p.n = __shfl_sync(0xffffffffu, l_n, s & 31);
+    p.ctx = __shfl_sync(0xffffffffu, l_ctx, s & 31);
+    p.t0 = tile;
+    p.t1 = (int)min((int64_t)tiles, tile + left);
+    left -= p.t1 - p.t0;
+    tile = p.t1;
+    return true;
+  }
+};
+
+// Exclusive sum of x over the CTA's threads in order, and the total.
+template <int W>
+__device__ __forceinline__ int64_t scan1(int64_t x, int64_t& total, int64_t* sw) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t i = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, i, o);
+    if (lane >= o) i += v;
+  }
+  if (lane == 31) sw[warp] = i;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += sw[w];
+    total += sw[w];
+  }
+  __syncthreads();
+  return before + i - x;
+}
+
+// One mask word pair of a row's view of a key tile: bit e of the result: the row sees key
+// t0 + e. Keys before `base` are seen, keys at or behind ctx are not.
+__device__ __forceinline__ uint64_t tile_view(const TreeArgs& a, int64_t row, int t0, int base,
+                                              int ctx) {
+  const int below = min(max(base - t0, 0), kKeys);   // keys of the committed context
+  uint64_t v = below >= 64 ? ~0ull : ((1ull << below) - 1ull);
+  if (below < kKeys) {
+    // draft bits from index t0 + below - base on, placed at bit `below`
+    const uint32_t* m = a.tree_mask + row * a.mask_words;
+    const int j0 = t0 + below - base;
+    uint64_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int w = (j0 >> 5) + k;
+      const uint64_t x = w < a.mask_words ? m[w] : 0u;
+      const int sh = 32 * k - (j0 & 31);
+      bits |= sh >= 64 ? 0ull : (sh >= 0 ? x << sh : x >> -sh);
+    }
+    v |= bits << below;
+    const int live = ctx - t0;
+    if (live < kKeys) v &= (1ull << live) - 1ull;
+  }
+  return v;
+}
+
+template <int BS, pa_dtype KV>
+__global__ void __launch_bounds__(Layout<KV != PA_BF16>::kThreads, 2)
+tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUtensorMap qmap,
+               const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  constexpr bool QUANT = KV != PA_BF16;
+  using L = Layout<QUANT>;
+  constexpr int kThreads = L::kThreads, W = kThreads / 32;
+  constexpr int NB = kKeys / BS;           // blocks of a key tile
+  constexpr int WT = 32 / NB;              // tiles of a window of 32 blocks
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.group, TM = kRows / G, Hkv = a.num_kv_heads;
+  const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK);
+  const uint32_t sV = smem_u32(smem + L::kOffV);
+  const uint32_t bar0 = smem_u32(smem + L::kOffBar);
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  TileInfo* info = reinterpret_cast<TileInfo*>(smem + L::kOffInfo);
+  int64_t* s_scan = reinterpret_cast<int64_t*>(smem + L::kOffMisc);          // [8]
+  int* s_start = reinterpret_cast<int*>(s_scan + 8);                        // rt, s, kvh, tile
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_start + 4);
+  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // drafts of the current piece whose V row holds a NaN or infinity, by draft index
+  // (two lists, for even and odd pieces: the converters may be one piece ahead)
+  uint32_t* s_odd = reinterpret_cast<uint32_t*>(tmem_slot + 2);              // [2][8]
+  volatile int* any_odd = reinterpret_cast<volatile int*>(s_odd + 16);       // [2]
+
+  pdl_wait();
+  if (tid == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      uint32_t count = 1;
+      if (i == L::kBarP || i == L::kBarP + 1 || i == L::kBarSm) count = kRows;
+      if (QUANT && ((i >= L::kBarKF && i < L::kBarKF + L::kKSt) ||
+                    (i >= L::kBarVF && i < L::kBarVF + L::kVSt) ||
+                    (i >= L::kBarK8E && i < L::kBarK8E + L::kK8St) ||
+                    (i >= L::kBarV8E && i < L::kBarV8E + L::kV8St)))
+        count = 32;  // one converter warp
+      mbar_init(bar(i), count);
+    }
+    *dead = 0;
+    for (int i = 0; i < 16; ++i) s_odd[i] = 0;
+    any_odd[0] = any_odd[1] = 0;
+    s_start[0] = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  // ---- the batch's key tiles, and where this CTA's run begins ----
+  const int rts = row_tiles_of(a.max_query_len, G);
+  const int seqs_per = (a.num_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(a.num_seqs, tid * seqs_per), s1 = min(a.num_seqs, s0 + seqs_per);
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    int q0, n, ctx;
+    if (seq_range(a, s, q0, n, ctx)) mine += (int64_t)row_tiles_of(n, G) * tiles_of(ctx);
+    else if (blockIdx.x == 0) flag_error(PA_DEVERR_QUERY);
+  }
+  int64_t total;
+  scan1<W>(mine, total, s_scan);
+  total *= Hkv;
+  const int64_t per = (total + kStreams - 1) / kStreams;
+  const int64_t w0 = per * blockIdx.x, count = min(per, total - w0);
+  if (count <= 0) {
+    if (tid == 0) ws.runs[blockIdx.x].tiles = 0;
+    return;
+  }
+  int64_t done = 0;
+  for (int rt = 0; rt < rts; ++rt) {
+    int64_t sum = 0;
+    for (int s = s0; s < s1; ++s) {
+      int q0, n, ctx;
+      if (seq_range(a, s, q0, n, ctx) && row_tiles_of(n, G) > rt) sum += tiles_of(ctx);
+    }
+    int64_t all;
+    int64_t at = scan1<W>(sum, all, s_scan);
+    if (w0 < done + all * Hkv) {
+      at = done + at * Hkv;
+      if (w0 >= at && w0 < at + sum * Hkv) {  // one thread's sequences hold it
+        for (int s = s0; s < s1; ++s) {
+          int q0, n, ctx;
+          if (!seq_range(a, s, q0, n, ctx) || row_tiles_of(n, G) <= rt) continue;
+          const int nt = tiles_of(ctx);
+          if (w0 < at + (int64_t)nt * Hkv) {
+            const int h = (int)((w0 - at) / nt);
+            s_start[0] = rt;
+            s_start[1] = s;
+            s_start[2] = h;
+            s_start[3] = (int)(w0 - at - (int64_t)h * nt);
+            ws.runs[blockIdx.x] = RunInfo{per, at + (int64_t)h * nt, rt, s, h, nt};
+            break;
+          }
+          at += (int64_t)nt * Hkv;
+        }
+      }
+      break;
+    }
+    done += all * Hkv;
+  }
+  if (warp == 0) {
+    pf::tmem_alloc(smem_u32(tmem_slot), kCols);
+    pf::tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk;
+  walk.start(a, s_start[0] >= 0 ? count : 0, s_start[0], s_start[1], s_start[2], s_start[3]);
+  // waits are made warp-uniform
+  auto wait_all = [&](uint32_t b, uint32_t parity) {
+    const bool w = !*dead && mbar_wait(b, parity);
+    return __all_sync(0xffffffffu, w) != 0;
+  };
+
+  if (warp == kTmaWarp) {
+    // ------------------------------ producer ------------------------------
+    // A window is up to 32 consecutive blocks of a piece, lane b holding block b.
+    struct Window {
+      int p;             // block id; -1: unreadable or none
+      float ks, vs;
+      int kz, vz;
+      int tile0, ntiles; // its key tiles within the piece
+      int kvh, q_tok, ctx;
+      bool first, any;   // first of its piece; exists
+    };
+    Piece pc;
+    bool have = walk.next(a, pc);
+    int wt = have ? pc.t0 : 0;
+    bool fresh = true;
+    auto next_window = [&](Window& w) {
+      w.any = have;
+      if (!have) return;
+      w.first = fresh;
+      w.tile0 = wt;
+      w.ntiles = min(WT, pc.t1 - wt);
+      w.kvh = pc.kvh;
+      w.q_tok = pc.q0 + pc.rt * TM;
+      w.ctx = pc.ctx;
+      w.p = -1;
+      w.ks = w.vs = 1.f;
+      w.kz = w.vz = 0;
+      const int blk = wt * NB + lane;
+      if (lane < w.ntiles * NB && blk * BS < pc.ctx) {
+        int p = a.block_tables[(int64_t)pc.s * a.max_blocks_per_seq + blk];
+        if (p < 0 || p >= a.num_blocks) {
+          flag_error(PA_DEVERR_BLOCK_ID);
+          p = -1;
+        } else if constexpr (QUANT) {
+          const int64_t bh = (int64_t)p * Hkv + pc.kvh;
+          w.ks = a.k_scales[bh];
+          w.vs = a.v_scales[bh];
+          if constexpr (KV == PA_INT8) {
+            w.kz = a.k_zeros[bh];
+            w.vz = a.v_zeros[bh];
+            if (!zero_in_range(w.kz) || !zero_in_range(w.vz)) {
+              flag_error(PA_DEVERR_ZERO);
+              p = -1;
+            }
+          }
+        }
+        w.p = p;
+      }
+      wt += w.ntiles;
+      fresh = false;
+      if (wt == pc.t1) {
+        have = walk.next(a, pc);
+        wt = have ? pc.t0 : 0;
+        fresh = true;
+      }
+    };
+    Window cur, nxt;
+    next_window(cur);
+    next_window(nxt);
+    const uint64_t keep = tc::evict_first_policy();
+    int g = 0, pieces = 0;
+    bool ok = true;
+    while (ok && cur.any) {
+      if (cur.first) {
+        // the last S product of the piece before has read Q
+        if (pieces > 0) ok = wait_all(bar(L::kBarQE), (pieces - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_tx(bar(L::kBarQF), kQBytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            pf::tma_load_4d(sQ + h * kQSlab, &qmap, 0, h, cur.kvh * G, cur.q_tok, bar(L::kBarQF),
+                            keep);
+        }
+        __syncwarp();
+        ++pieces;
+      }
+      for (int k = 0; k < cur.ntiles; ++k, ++g) {
+        // this tile's blocks sit in lanes k * NB ..
+        const int src = (k * NB + (lane & (NB - 1))) & 31;
+        const int p = __shfl_sync(0xffffffffu, cur.p, src);
+        const bool exists = (cur.tile0 + k) * kKeys + (lane & (NB - 1)) * BS < cur.ctx;
+        const uint32_t good = __ballot_sync(0xffffffffu, lane < NB && p >= 0);
+        const uint32_t bad = __ballot_sync(0xffffffffu, lane < NB && p < 0 && exists);
+        const float ks = __shfl_sync(0xffffffffu, cur.ks, src), vs = __shfl_sync(0xffffffffu, cur.vs, src);
+        const int kz = __shfl_sync(0xffffffffu, cur.kz, src), vz = __shfl_sync(0xffffffffu, cur.vz, src);
+        const int pb = __shfl_sync(0xffffffffu, p, (lane >> 1) & (NB - 1));
+        // ---- K, then V: the ring's stage is free once its last reader is done ----
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int nst = QUANT ? (kv ? L::kV8St : L::kK8St) : (kv ? L::kVSt : L::kKSt);
+          const int full = QUANT ? (kv ? L::kBarV8F : L::kBarK8F) : (kv ? L::kBarVF : L::kBarKF);
+          const int empty = QUANT ? (kv ? L::kBarV8E : L::kBarK8E) : (kv ? L::kBarVE : L::kBarKE);
+          const int st = g % nst;
+          if (g >= nst) ok = wait_all(bar(empty + st), ((g / nst) - 1) & 1);
+          if (!ok) break;
+          if (kv == 0) {
+            // The slot is free: the stage's K (bf16) or codes (two tiles' conversions later)
+            // could only be read after S(g - 4) at the earliest, which was issued behind
+            // P V (g - 6), so softmax and converters are past tile g - 6 > g - kInfo.
+            TileInfo& ti = info[g % kInfo];
+            if (lane == 0) ti.bad = bad;
+            if (QUANT && lane < NB) {
+              ti.ks[lane] = ks;
+              ti.vs[lane] = vs;
+              ti.kz[lane] = kz;
+              ti.vz[lane] = vz;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kBarInfo + g % kInfo));
+          }
+          const uint32_t fb = bar(full + st);
+          if (lane == 0)
+            mbar_arrive_tx(fb, (uint32_t)__popc(good) * BS * 128u * (QUANT ? 1u : 2u));
+          __syncwarp();
+          if constexpr (QUANT) {
+            if (lane < NB && p >= 0)
+              tc::tma_load_2d(smem_u32(smem + (kv ? L::kOffV8 : L::kOffK8)) + st * kCodeBytes +
+                                  lane * BS * 128,
+                              kv ? &vmap : &kmap, 0, (p * Hkv + cur.kvh) * BS, fb, keep);
+          } else {
+            if (lane < 2 * NB && pb >= 0)
+              pf::tma_load_3d((kv ? sV : sK) + st * kKVBytes + (lane & 1) * kKVSlab +
+                                  (lane >> 1) * BS * 128,
+                              kv ? &vmap : &kmap, 0, lane & 1, (pb * Hkv + cur.kvh) * BS, fb);
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok) break;
+      cur = nxt;
+      next_window(nxt);
+    }
+    if (!ok) {
+      if (lane == 0) {
+        flag_error(PA_DEVERR_TIMEOUT);
+        *dead = 1;
+      }
+      __syncwarp();
+      // copies in flight complete (each barrier's last phase) before shared memory is released
+      if (lane == 0) {
+        if (pieces > 0) mbar_wait(bar(L::kBarQF), (pieces - 1) & 1);
+        for (int kv = 0; kv < 2; ++kv) {
+          const int nst = QUANT ? (kv ? L::kV8St : L::kK8St) : (kv ? L::kVSt : L::kKSt);
+          const int full = QUANT ? (kv ? L::kBarV8F : L::kBarK8F) : (kv ? L::kBarVF : L::kBarKF);
+          for (int j = max(0, g - nst); j <= g; ++j)
+            mbar_wait(bar(full + j % nst), (j / nst) & 1);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------ MMA issuer ------------------------------
+    Piece pc;
+    auto issue_s = [&](int g) {
+      const uint32_t kst = sK + (g % L::kKSt) * kKVBytes;
+#pragma unroll
+      for (int kk = 0; kk < kDim / 16; ++kk)
+        pf::umma_bf16(tmem + (g & 1) * kKeys,
+                      sdesc(sQ + (kk >> 2) * kQSlab + (kk & 3) * 32, 16, 1024),
+                      sdesc(kst + (kk >> 2) * kKVSlab + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0);
+      umma_commit(bar(L::kBarSF + (g & 1)));
+      umma_commit(bar(L::kBarKE + g % L::kKSt));
+    };
+    auto issue_pv = [&](int g, bool fresh) {
+      const uint32_t vst = sV + (g % L::kVSt) * kKVBytes;
+#pragma unroll
+      for (int kk = 0; kk < kKeys / 16; ++kk)
+        pf::umma_bf16_ts(tmem + kOCol, tmem + (g & 1) * kKeys + kk * 8,
+                         sdesc(vst + kk * 16 * 128, kKVSlab, 1024), kIdescPV, !fresh || kk > 0);
+      umma_commit(bar(L::kBarO + (g & 1)));
+      umma_commit(bar(L::kBarVE + g % L::kVSt));
+    };
+    int g = 0, pieces = 0;      // tiles whose S is issued; pieces whose Q is in use
+    int left = 0;               // tiles of the current piece whose S is not issued
+    bool ok = true, fresh_s = false;
+    bool fresh_pv[2] = {true, true};
+    // S of the next tile of the run; false when there is none (or a wait gave up)
+    auto next_s = [&]() {
+      if (left == 0) {
+        if (!walk.next(a, pc)) return false;
+        left = pc.t1 - pc.t0;
+        fresh_s = true;
+        ok = wait_all(bar(L::kBarQF), pieces & 1);
+        if (!ok) return false;
+        ++pieces;
+      }
+      ok = wait_all(bar(L::kBarKF + g % L::kKSt), (g / L::kKSt) & 1);
+      if (!ok) return false;
+      tc_fence_after();
+      fresh_pv[g & 1] = fresh_s;
+      fresh_s = false;
+      --left;
+      if (lane == 0) {
+        issue_s(g);
+        if (left == 0) umma_commit(bar(L::kBarQE));
+      }
+      __syncwarp();
+      ++g;
+      return true;
+    };
+    bool more = next_s();
+    for (int j = 0; ok && more; ++j) {
+      more = next_s();
+      if (!ok) break;
+      ok = wait_all(bar(L::kBarP + (j & 1)), (j >> 1) & 1) &&
+           wait_all(bar(L::kBarVF + j % L::kVSt), (j / L::kVSt) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) issue_pv(j, fresh_pv[j & 1]);
+      __syncwarp();
+      more = j + 1 < g;
+    }
+    if (lane == 0) {
+      if (!ok) {
+        flag_error(PA_DEVERR_TIMEOUT);
+        *dead = 1;
+      }
+      // every product of the CTA completes before tensor memory is released
+      umma_commit(bar(L::kBarFin));
+      mbar_wait(bar(L::kBarFin), 0);
+    }
+    __syncwarp();
+  } else if (QUANT && warp >= kConvWarp) {
+    // ------------------------------ converters ------------------------------
+    // Warp 6 turns K tiles, warp 7 V tiles. A lane takes 16 codes at a time: value = the E4M3
+    // code's value or code - zero, exact in bf16, stored where TMA would put bf16 (128-byte
+    // rows of 64 channels, 16-byte chunks XORed with row % 8). V rows that cannot be read or
+    // lie behind the context become zero, and so do NaN codes of drafts: P is zero for rows
+    // that do not see them, but 0 * NaN is not (rows that see one get it back at the end).
+    const int kv = warp - kConvWarp;
+    const int nst = kv ? L::kVSt : L::kKSt, nst8 = kv ? L::kV8St : L::kK8St;
+    Piece pc;
+    int g = 0, par = 1;
+    bool ok = true;
+    while (ok && walk.next(a, pc)) {
+      par ^= 1;
+      for (int t = pc.t0; t < pc.t1 && ok; ++t, ++g) {
+        const int st = g % nst, st8 = g % nst8;
+        ok = wait_all(bar(L::kBarInfo + g % kInfo), (g / kInfo) & 1) &&
+             wait_all(bar((kv ? L::kBarV8F : L::kBarK8F) + st8), (g / nst8) & 1);
+        if (ok && g >= nst)
+          ok = wait_all(bar((kv ? L::kBarVE : L::kBarKE) + st), ((g / nst) - 1) & 1);
+        if (!ok) break;
+        const TileInfo& ti = info[g % kInfo];
+        const uint8_t* src = smem + (kv ? L::kOffV8 + st8 * kCodeBytes : L::kOffK8 + st8 * kCodeBytes);
+        const uint32_t dst = (kv ? sV : sK) + st * kKVBytes;
+        const int live = pc.ctx - t * kKeys, base = pc.ctx - pc.n;
+        const uint32_t bad = ti.bad;
+#pragma unroll 4
+        for (int it = 0; it < kKeys * 8 / 32; ++it) {
+          const int key = it * 4 + (lane >> 3), q8 = lane & 7;
+          const uint4 raw = *reinterpret_cast<const uint4*>(src + key * 128 + q8 * 16);
+          const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
+          uint32_t o[8];
+          const float z = KV == PA_INT8 ? (float)(kv ? ti.vz[key / BS] : ti.kz[key / BS]) : 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float f[4];
+            if constexpr (KV == PA_INT8) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(wd[k] >> (8 * e)) - z;
+            } else {
+              pf::f16x2_to_f32(e4m3x2_to_f16x2((uint16_t)(wd[k] & 0xffffu)), f[0], f[1]);
+              pf::f16x2_to_f32(e4m3x2_to_f16x2((uint16_t)(wd[k] >> 16)), f[2], f[3]);
+            }
+            o[2 * k] = pack_bf16x2(f[0], f[1]);
+            o[2 * k + 1] = pack_bf16x2(f[2], f[3]);
+          }
+          if (kv) {
+            const bool gone = key >= live || ((bad >> (key / BS)) & 1u);
+            if (gone) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = 0;
+            } else if (KV == PA_FP8_E4M3 && t * kKeys + key >= base) {
+              bool odd = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (((wd[k] >> (8 * e)) & 0x7fu) == 0x7fu) {
+                    odd = true;
+                    o[2 * k + (e >> 1)] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+                  }
+              if (odd) {
+                const int j = t * kKeys + key - base;
+                atomicOr(&s_odd[par * 8 + (j >> 5)], 1u << (j & 31));
+                any_odd[par] = 1;
+              }
+            }
+          }
+          const uint32_t row = dst + (q8 >> 2) * kKVSlab + key * 128;
+          const int c0 = 2 * (q8 & 3);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       ::"r"(row + ((c0 ^ (key & 7)) << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                         "r"(o[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       ::"r"(row + (((c0 + 1) ^ (key & 7)) << 4)), "r"(o[4]), "r"(o[5]),
+                         "r"(o[6]), "r"(o[7]) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(bar((kv ? L::kBarV8E : L::kBarK8E) + st8));
+        mbar_arrive(bar((kv ? L::kBarVF : L::kBarKF) + st));
+      }
+    }
+    if (!ok && lane == 0) {
+      flag_error(PA_DEVERR_TIMEOUT);
+      *dead = 1;
+    }
+  } else if (warp < 4) {
+    // ------------------------------ softmax ------------------------------
+    const int r = tid;                                 // row of the tile = tensor-memory lane
+    const int tok = r / G, head = r - tok * G;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const float sl2 = a.scale_log2;
+    Piece pc;
+    int g = 0;
+    bool ok = true;
+    bool first_piece = true;
+    int par = 1;
+    uint32_t syncs = 0;
+    // the four warps meet, within a bound (one of them may have given up)
+    auto meet = [&]() {
+      mbar_arrive(bar(L::kBarSm));
+      return wait_all(bar(L::kBarSm), syncs++ & 1);
+    };
+    while (ok && walk.next(a, pc)) {
+      par ^= 1;
+      const int rows = min(TM, pc.n - pc.rt * TM);     // tokens of the tile
+      const bool live_row = tok < rows;
+      const bool live_warp = warp * 32 < rows * G;
+      const int64_t row = pc.q0 + pc.rt * TM + min(tok, rows - 1);
+      const int base = pc.ctx - pc.n;
+      float m_used = -INFINITY, l = 0.f;
+      for (int t = pc.t0; t < pc.t1; ++t, ++g) {
+        const int t0 = t * kKeys, live = pc.ctx - t0;
+        const uint32_t sbuf = lanes + (g & 1) * kKeys;
+        ok = wait_all(bar(L::kBarInfo + g % kInfo), (g / kInfo) & 1) &&
+             wait_all(bar(L::kBarSF + (g & 1)), (g >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const TileInfo& ti = info[g % kInfo];
+        const uint32_t bad = ti.bad;
+        if (live_warp) {
+          uint32_t sv[2][32];
+          tmem_ld32(sbuf, sv[0]);
+          tmem_ld32(sbuf + 32, sv[1]);
+          tmem_wait_ld(sv[0]);
+          tmem_wait_ld(sv[1]);
+          // scores in the log2 domain (with the K scale of their block), then the mask
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float f = QUANT ? sl2 * ti.ks[(c * 32 + e) / BS] : sl2;
+              sv[c][e] = __float_as_uint(__uint_as_float(sv[c][e]) * f);
+            }
+          if (t0 + kKeys > base || bad != 0) {
+            uint64_t v = tile_view(a, row, t0, base, pc.ctx);
+            if (bad != 0) {
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                if ((bad >> b) & 1u) v &= ~(((1ull << BS) - 1ull) << (b * BS));
+            }
+            const uint32_t v2[2] = {(uint32_t)v, (uint32_t)(v >> 32)};
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((v2[c] >> e) & 1u)) sv[c][e] = 0xff800000u;  // -inf
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[c][e]));
+          const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          float alpha = 1.f;
+          if (m_new > m_used + 8.f) {  // lazy: P stays at or below 2^8 otherwise
+            alpha = fast_exp2(m_used - m_new);
+            m_used = m_new;
+          }
+          const float mref = m_used == -INFINITY ? 0.f : m_used;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float p0 = fast_exp2(__uint_as_float(sv[c][e]) - mref);
+              float p1 = fast_exp2(__uint_as_float(sv[c][e + 1]) - mref);
+              sum[e & 3] += p0;
+              sum[(e + 1) & 3] += p1;
+              if constexpr (QUANT) {  // P carries the V scale; a masked key carries none
+                const float vs = ti.vs[(c * 32 + e) / BS];
+                p0 = p0 == 0.f ? 0.f : p0 * vs;
+                p1 = p1 == 0.f ? 0.f : p1 * vs;
+              }
+              pk[c * 16 + (e >> 1)] = pack_bf16x2(p0, p1);
+            }
+          tmem_st32(sbuf, pk);
+          l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+          tmem_wait_st();
+          if (t > pc.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // O holds the tiles before this one once their last product is done
+            ok = wait_all(bar(L::kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(lanes + kOCol + c * 32, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(lanes + kOCol + c * 32, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        if constexpr (!QUANT) {
+          // V rows that cannot be read or lie behind the context may hold anything: zero
+          // them. A NaN or infinity in a draft's V row is taken out too (see the converters).
+          if (live < kKeys || bad != 0 || t0 + kKeys > base) {
+            ok = wait_all(bar(L::kBarVF + g % L::kVSt), (g / L::kVSt) & 1);
+            if (!ok) break;
+            const int key = r & (kKeys - 1);
+            const uint32_t vrow = sV + (g % L::kVSt) * kKVBytes + (r >> 6) * kKVSlab + key * 128;
+            if (key >= live || ((bad >> (key / BS)) & 1u)) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + k * 16), "r"(0)
+                             : "memory");
+            } else if (t0 + key >= base) {
+#pragma unroll 1
+              for (int k = 0; k < 32; ++k) {
+                const uint32_t addr = vrow + ((k + r) & 31) * 4;
+                uint32_t x;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+                const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
+                if (lo || hi) {
+                  x &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+                  const int j = t0 + key - base;
+                  atomicOr(&s_odd[par * 8 + (j >> 5)], 1u << (j & 31));
+                  any_odd[par] = 1;
+                }
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bar(L::kBarP + (g & 1)));
+      }
+      if (!ok) break;
+      // ---- the piece is done: O / l, or the partial ----
+      ok = wait_all(bar(L::kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      // rows that see a draft with a NaN or infinity in V get it back: the four warps have
+      // all written the list before one reads it, and read it before it is emptied
+      ok = meet();
+      if (!ok) break;
+      const bool odd = any_odd[par] != 0;
+      const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
+      const int64_t slot = (int64_t)blockIdx.x * 2 + (first_piece ? 0 : 1);
+      const int64_t orow = row * a.num_q_heads + pc.kvh * G + head;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      if (live_warp) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lanes + kOCol + c * 32, o);
+          tmem_wait_ld(o);
+          if (odd && live_row) {
+            for (int j = 0; j < pc.n; ++j) {
+              if (!((s_odd[par * 8 + (j >> 5)] >> (j & 31)) & 1u)) continue;
+              if (!((a.tree_mask[row * a.mask_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
+              const int key = base + j;
+              const int64_t blk = a.block_tables[(int64_t)pc.s * a.max_blocks_per_seq + key / BS];
+              const int64_t at = ((blk * Hkv + pc.kvh) * BS + key % BS) * kDim + c * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                float v = 0.f;
+                if constexpr (!QUANT) {
+                  v = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.v_cache)[at + e] << 16);
+                  if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) v = 0.f;
+                } else {
+                  if ((static_cast<const uint8_t*>(a.v_cache)[at + e] & 0x7f) == 0x7f)
+                    v = __uint_as_float(0x7fc00000u);
+                }
+                o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
+              }
+            }
+          }
+          if (live_row && whole) {
+            uint16_t* op = static_cast<uint16_t*>(a.out) + orow * kDim + c * 32;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 w;
+              w.x = pack_bf16x2(__uint_as_float(o[8 * k + 0]) * inv, __uint_as_float(o[8 * k + 1]) * inv);
+              w.y = pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv);
+              w.z = pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv);
+              w.w = pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv);
+              *reinterpret_cast<uint4*>(op + 8 * k) = w;
+            }
+          } else if (live_row) {
+            float4* ap = reinterpret_cast<float4*>(ws.acc) + (slot * (kDim / 4) + c * 8) * kRows + r;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              ap[k * kRows] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                          __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+          __syncwarp();
+        }
+        if (live_row) {
+          if (whole) {
+            if (a.lse_out != nullptr)
+              a.lse_out[orow] = l != 0.f ? (m_used + __log2f(l)) * kLn2 : -INFINITY;
+          } else {
+            ws.m[slot * kRows + r] = m_used;
+            ws.l[slot * kRows + r] = l;
+          }
+        }
+      }
+      if (odd) {
+        ok = meet();
+        if (!ok) break;
+        if (tid < 8) s_odd[par * 8 + tid] = 0;
+        if (tid == 0) any_odd[par] = 0;
+        ok = meet();
+        if (!ok) break;
+      }
+      tc_fence_before();  // O is read before the next P is handed over
+      first_piece = false;
+    }
+    if (!ok && lane == 0) {
+      flag_error(PA_DEVERR_TIMEOUT);
+      *dead = 1;
+    }
+  }
+
+  // ------------------------------ teardown ------------------------------
+  tc_fence_before();
+  __syncthreads();
+  pdl_trigger();
+  if (warp == 0) {
+    tc_fence_after();
+    pf::tmem_dealloc(tmem, kCols);
+  }
+}
+
+// Joins the pieces of every (row tile, sequence, kv head) that a cut falls into: grid (cuts,
+// 4 x 32 rows). The cut where it is first cut does the work; thread (warp w, lane) takes row
+// lane of the group and channels 32 w .. 32 w + 31, pieces in order. Few cuts (at most
+// kStreams - 1), so it is bound by two dependent reads per piece.
+__global__ void __launch_bounds__(128) tree_tc_reduce_kernel(const TreeArgs a, const Workspace ws) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x + 1;
+  const RunInfo run = ws.runs[b];
+  if (run.tiles == 0 || run.begin == run.per * b) return;    // no run, or cut between two
+  const int first = (int)(run.begin / run.per);
+  if (first != b - 1) return;
+  const int last = (int)((run.begin + run.tiles - 1) / run.per);
+  const int G = a.group, TM = kRows / G;
+  const int q0 = a.query_start[run.s], n = a.query_start[run.s + 1] - q0;
+  const int rows = min(TM, n - run.rt * TM) * G;
+  const int r = 32 * blockIdx.y + (threadIdx.x & 31), w = threadIdx.x >> 5;
+  if (r >= rows) return;
+  auto slot_of = [&](int k) {
+    return (int64_t)k * 2 + (k == first && run.begin != run.per * first ? 1 : 0);
+  };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int k = first; k <= last; ++k) M = fmaxf(M, ws.m[slot_of(k) * kRows + r]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  float4 acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = first; k <= last; ++k) {
+    const int64_t slot = slot_of(k);
+    const float f = fast_exp2(ws.m[slot * kRows + r] - ref);
+    L = fmaf(f, ws.l[slot * kRows + r], L);
+    const float4* src = reinterpret_cast<const float4*>(ws.acc) + (slot * (kDim / 4) + 8 * w) * kRows + r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 v = src[j * kRows];
+      acc[j].x = fmaf(f, v.x, acc[j].x);
+      acc[j].y = fmaf(f, v.y, acc[j].y);
+      acc[j].z = fmaf(f, v.z, acc[j].z);
+      acc[j].w = fmaf(f, v.w, acc[j].w);
+    }
+  }
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  const int64_t row = (int64_t)(q0 + run.rt * TM + r / G) * a.num_q_heads + run.kvh * G + r % G;
+  uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * kDim + 32 * w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 x = acc[2 * j], y = acc[2 * j + 1];
+    op[j] = make_uint4(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv),
+                       pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+  }
+  if (w == 0 && a.lse_out != nullptr)
+    a.lse_out[row] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int BS, pa_dtype KV>
+inline cudaError_t launch_bs(const TreeArgs& a, const Workspace& ws, cudaStream_t st) {
+  using L = Layout<KV != PA_BF16>;
+  CUtensorMap qm, km, vm;
+  const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * BS;
+  const bool maps = KV == PA_BF16 ? pf::make_kv_map(&km, a.k_cache, rows, BS) &&
+                                        pf::make_kv_map(&vm, a.v_cache, rows, BS)
+                                  : pf::make_kv8_map(&km, a.k_cache, rows, BS) &&
+                                        pf::make_kv8_map(&vm, a.v_cache, rows, BS);
+  if (!maps || !pf::make_q_map(&qm, a.q, a.num_tokens, a.num_q_heads, a.group))
+    return cudaErrorInvalidValue;
+  static tc::DeviceCache slots;
+  int per_sm = 0;
+  cudaError_t e = tc::resident_per_sm(tree_tc_kernel<BS, KV>, L::kThreads, L::kSmem, slots, &per_sm);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(tree_tc_kernel<BS, KV>, dim3(kStreams), dim3(L::kThreads), L::kSmem, st, a, ws,
+                 qm, km, vm);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_tc_reduce_kernel, dim3(kStreams - 1, kRows / 32), dim3(128), 0, st, a, ws);
+}
+
+inline cudaError_t launch_tc(const TreeArgs& a, pa_dtype kv, const Workspace& ws, cudaStream_t st) {
+  auto by_bs = [&](auto kvc) -> cudaError_t {
+    constexpr pa_dtype KV = decltype(kvc)::value;
+    if (a.block_size == 8) return launch_bs<8, KV>(a, ws, st);
+    if (a.block_size == 32) return launch_bs<32, KV>(a, ws, st);
+    return launch_bs<16, KV>(a, ws, st);
+  };
+  if (kv == PA_FP8_E4M3) return by_bs(std::integral_constant<pa_dtype, PA_FP8_E4M3>{});
+  if (kv == PA_INT8) return by_bs(std::integral_constant<pa_dtype, PA_INT8>{});
+  return by_bs(std::integral_constant<pa_dtype, PA_BF16>{});
+}
+
+}  // namespace tree
+}  // namespace pa
