@@ -2,6 +2,7 @@
 // and one kernel-family setting): decode, prefill and cache entry points (pagedattn.cu), and
 // those of a drafted step. Declarations and contracts: include/pagedattn.h.
 #include <algorithm>
+#include <initializer_list>
 
 #include "pagedattn.cu"
 
@@ -12,6 +13,26 @@
 
 namespace pa {
 namespace {
+
+// Memory of one buffer of a call; `out`: the call writes it.
+struct Span {
+  const void* p;
+  int64_t bytes;
+  bool out;
+};
+
+// Whether no output shares memory with another buffer (absent ones have no pointer).
+bool apart(std::initializer_list<Span> all) {
+  for (const Span& a : all) {
+    if (!a.out || a.p == nullptr) continue;
+    const char* a0 = static_cast<const char*>(a.p);
+    for (const Span& b : all) {
+      const char* b0 = static_cast<const char*>(b.p);
+      if (&a != &b && b0 != nullptr && a0 < b0 + b.bytes && b0 < a0 + a.bytes) return false;
+    }
+  }
+  return true;
+}
 
 // Parts of the context on the CUDA-core path: enough CTAs for about eight per SM, at most
 // one part per 512 tokens (below that the joining costs more than the split gives).
@@ -102,8 +123,13 @@ pa_status paged_build_step(const int32_t* context_lens, const int32_t* new_lens,
       (max_tokens > 0 && !slot_mapping))
     return PA_ERR_INVALID;
   // every CTA reads the inputs while the first writes the outputs
-  if (blocks_held_out == blocks_held || queue_state_out == queue_state ||
-      total_lens == context_lens || total_lens == new_lens || blocks_held_out == context_lens)
+  const int64_t S4 = 4 * (int64_t)num_seqs, T4 = 4 * (int64_t)max_tokens;
+  if (!apart({{context_lens, S4, false}, {new_lens, S4, false}, {blocks_held, S4, false},
+              {parents, T4, false}, {block_tables, S4 * max_blocks_per_seq, true},
+              {free_blocks, 4 * (int64_t)free_capacity, false}, {queue_state, 8, false},
+              {total_lens, S4, true}, {query_start, S4 + 4, true}, {blocks_held_out, S4, true},
+              {queue_state_out, 8, true}, {slot_mapping, 2 * T4, true}, {positions, T4, true},
+              {tree_mask, T4 * mask_words, true}, {status, 4, true}}))
     return PA_ERR_INVALID;
   const step::BuildArgs a{context_lens, new_lens, blocks_held, parents, block_tables, free_blocks,
                           queue_state, total_lens, query_start, blocks_held_out, queue_state_out,
@@ -130,8 +156,11 @@ pa_status paged_release_blocks(const int32_t* keep_lens, const int32_t* blocks_h
   if (!keep_lens || !blocks_held || !block_tables || !free_blocks || !queue_state ||
       !blocks_held_out || !queue_state_out)
     return PA_ERR_INVALID;
-  if (blocks_held_out == blocks_held || queue_state_out == queue_state ||
-      blocks_held_out == keep_lens)
+  const int64_t S4 = 4 * (int64_t)num_seqs;
+  if (!apart({{keep_lens, S4, false}, {blocks_held, S4, false},
+              {block_tables, S4 * max_blocks_per_seq, false},
+              {free_blocks, 4 * (int64_t)free_capacity, true}, {queue_state, 8, false},
+              {blocks_held_out, S4, true}, {queue_state_out, 8, true}, {status, 4, true}}))
     return PA_ERR_INVALID;
   // 64 sequences per CTA, more when that would be over one CTA per SM (148 of them)
   const int per = std::max(64, (num_seqs + 147) / 148);
@@ -179,7 +208,12 @@ pa_status rotary_and_cache(const void* q, const void* k, const void* v, void* q_
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) ||
       !aligned16(v_cache))
     return PA_ERR_INVALID;
-  if (q_out == q && d.q_out_stride != d.q_stride) return PA_ERR_INVALID;
+  // q_out is q or lies apart from it
+  const int64_t es = dtype_bytes(d.in_dtype), more = d.num_tokens - 1;
+  if (q_out == q ? d.q_out_stride != d.q_stride
+                 : !apart({{q, (more * d.q_stride + qrow) * es, false},
+                           {q_out, (more * d.q_out_stride + qrow) * es, true}}))
+    return PA_ERR_INVALID;
   const bool quant = d.cache_dtype == PA_FP8_E4M3 || d.cache_dtype == PA_INT8;
   if (quant && (!k_scales || !v_scales)) return PA_ERR_INVALID;
   if (d.cache_dtype == PA_INT8 && (!k_zeros || !v_zeros)) return PA_ERR_INVALID;
@@ -294,6 +328,12 @@ pa_status tree_verify(const int32_t* parents, const int64_t* draft_tokens,
   if (num_seqs == 0) return PA_OK;
   if ((num_tokens > 0 && (!parents || !draft_tokens || !target_tokens)) || !query_start ||
       !context_lens || !accepted || !num_accepted || !next_tokens || !kept_lens)
+    return PA_ERR_INVALID;
+  const int64_t S4 = 4 * (int64_t)num_seqs, T4 = 4 * (int64_t)num_tokens;
+  if (!apart({{parents, T4, false}, {draft_tokens, 2 * T4, false}, {target_tokens, 2 * T4, false},
+              {query_start, S4 + 4, false}, {context_lens, S4, false},
+              {accepted, S4 * max_accept, true}, {num_accepted, S4, true},
+              {next_tokens, 2 * S4, true}, {kept_lens, S4, true}}))
     return PA_ERR_INVALID;
   const step::VerifyArgs a{parents, draft_tokens, target_tokens, query_start, context_lens,
                            accepted, num_accepted, next_tokens, kept_lens, num_seqs, num_tokens,

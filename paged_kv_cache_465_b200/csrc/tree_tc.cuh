@@ -25,7 +25,7 @@
 //                memory while S(g) is in softmax, then O += P(g) V, P read from tensor memory;
 //   warps 0-3    softmax, one thread per row (= tensor-memory lane): mask, running maximum
 //                with lazy rescaling, P as bf16 pairs over S; O / l or the partial at the end;
-//   warps 6, 7   fp8 / int8 caches: turn the codes that TMA staged into the bf16 tiles the
+//   warps 6-9    fp8 / int8 caches: turn the codes that TMA staged into the bf16 tiles the
 //                products read (exact values; scales go to the scores and to P).
 // Two CTAs per SM hide each other's starts, ends and waits.
 //
@@ -50,16 +50,31 @@ using pf::umma_commit;
 using tc::mbar_arrive;
 using tc::mbar_arrive_tx;
 using tc::mbar_init;
-using tc::mbar_wait;
 using tc::smem_u32;
+
+// Bounded wait for the phase with the given parity: false after 2^22 polls (a poll that waits
+// is itself suspended by the hardware for a while). Kept this short because the kernel has
+// dozens of waits and its speed hangs on its code fitting the instruction cache.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  bool done = tc::mbar_try_wait(bar, parity);
+#pragma unroll 1
+  for (int i = 0; !done && i < (1 << 22); ++i) done = tc::mbar_try_wait(bar, parity);
+  return done;
+}
 
 constexpr int kRows = 128;                 // rows of a tile
 constexpr int kKeys = 64;                  // keys of a tile
 constexpr int kDim = 128;
 constexpr int kStreams = 296;              // runs the batch is cut into: two CTAs per SM of 148
+// What a piece costs beside its key tiles (Q, first scores, last products, output), in key
+// tiles: short contexts would otherwise pile up in few runs.
+#ifndef PA_TREE_PIECE_COST
+#define PA_TREE_PIECE_COST 4
+#endif
+constexpr int kPieceCost = PA_TREE_PIECE_COST;
 constexpr int kMmaWarp = 4, kTmaWarp = 5, kConvWarp = 6;
-constexpr int kQSlab = kRows * 128;        // 64 channels (128 B) x 128 rows
-constexpr int kQBytes = 2 * kQSlab;
+constexpr int kConvWarps = 2;              // converter warps for K, and as many for V
+constexpr int kQBytes = 2 * kRows * 128;   // Q: one tile of 128 rows, or two of up to 64
 constexpr int kKVSlab = kKeys * 128;       // 64 channels x 64 keys
 constexpr int kKVBytes = 2 * kKVSlab;
 constexpr int kCodeBytes = kKeys * 128;    // one-byte codes of 64 keys
@@ -68,16 +83,24 @@ constexpr int kInfo = 8;                   // ring of per-tile facts for softmax
 constexpr uint32_t kCols = 256;            // tensor memory: S at 0 and 64 (P over it), O at 128
 constexpr uint32_t kOCol = 128;
 
-// What the producer knows about a key tile.
+// A key tile as the producer describes it to the other warps (one slot of a ring): only the
+// producer walks the batch.
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kWhole = 8 };
 struct TileInfo {
-  uint32_t bad;                            // bit b: block b of the tile cannot be read
+  int flags;        // first / last tile of its piece; the run is over; the piece is a whole pair
+  uint32_t bad;     // bit b: block b of the tile cannot be read
+  int key0;         // position of the tile's first key
+  int base, ctx;    // context without and with the step's rows
+  int row0, rows;   // first token row of the row tile, its tokens
+  int s, kvh;
+  int slot;         // workspace slot of a partial piece
   float ks[kMaxTileBlocks], vs[kMaxTileBlocks];
   int kz[kMaxTileBlocks], vz[kMaxTileBlocks];
 };
 
 template <bool QUANT>
 struct Layout {
-  static constexpr int kThreads = QUANT ? 256 : 192;
+  static constexpr int kThreads = QUANT ? 192 + 64 * kConvWarps : 192;
   static constexpr int kKSt = QUANT ? 1 : 2;     // bf16 tiles of K and of V
   static constexpr int kVSt = QUANT ? 1 : 2;
   static constexpr int kK8St = QUANT ? 3 : 0;    // staged codes
@@ -91,8 +114,8 @@ struct Layout {
   static constexpr int kOffMisc = kOffInfo + kInfo * (int)sizeof(TileInfo);
   static constexpr int kOffBar = kOffMisc + 384;
   // barriers
-  static constexpr int kBarQF = 0, kBarQE = 1;
-  static constexpr int kBarKF = 2, kBarKE = kBarKF + kKSt;
+  static constexpr int kBarQF = 0, kBarQE = 2;   // [2] each
+  static constexpr int kBarKF = 4, kBarKE = kBarKF + kKSt;
   static constexpr int kBarVF = kBarKE + kKSt, kBarVE = kBarVF + kVSt;
   static constexpr int kBarSF = kBarVE + kVSt;   // [2] S in tensor memory
   static constexpr int kBarP = kBarSF + 2;       // [2] P in tensor memory
@@ -117,8 +140,8 @@ constexpr uint32_t kIdescPV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
 
 // Workspace: what CTA b's run is, then the partial pieces.
 struct RunInfo {
-  int64_t per;       // key tiles of a run
-  int64_t begin;     // first tile of the (row tile, sequence, kv head) that the run begins in
+  int64_t per;       // length of a run
+  int64_t begin;     // where the (row tile, sequence, kv head) that the run begins in begins
   int rt, s, kvh, tiles;  // that one, and its key tiles; tiles = 0: the run is empty
 };
 struct Workspace {
@@ -155,8 +178,10 @@ __device__ __forceinline__ int row_tiles_of(int n, int G) {
 // The pieces of a run in order, the same for every warp that walks it: 32 sequences' ranges
 // are held one per lane. All members but those are warp-uniform; every lane takes part.
 struct Walk {
-  int64_t left;
-  int rt, s, kvh, tile, tiles, base;
+  int64_t left;                // of the run
+  int rt, s, kvh, tiles, base;
+  int at;                      // place in the current (row tile, sequence, kv head): its first
+                               // kPieceCost places hold no tile
   int l_q0, l_n, l_ctx;  // this lane's sequence base + lane (n = 0: none, or nothing to do)
 
   __device__ __forceinline__ void load(const TreeArgs& a) {
@@ -165,12 +190,12 @@ struct Walk {
     if (k < a.num_seqs && !seq_range(a, k, l_q0, l_n, l_ctx)) l_n = 0;
   }
   __device__ __forceinline__ void start(const TreeArgs& a, int64_t count, int rt_, int s_, int kvh_,
-                                        int tile_) {
+                                        int at_) {
     left = count;
     rt = rt_;
     s = s_;
     kvh = kvh_;
-    tile = tile_;
+    at = at_;
     base = s & ~31;
     if (left > 0) {
       load(a);
@@ -178,45 +203,51 @@ struct Walk {
     }
   }
   __device__ __forceinline__ bool next(const TreeArgs& a, Piece& p) {
-    if (left <= 0) return false;
-    if (tile == tiles) {
-      tile = 0;
-      if (++kvh == a.num_kv_heads) {
-        kvh = 0;
-        int from = (s & 31) + 1;
-        while (true) {
-          const unsigned v = __ballot_sync(
-              0xffffffffu, (int)(threadIdx.x & 31) >= from && (int64_t)l_n * a.group > (int64_t)rt * kRows);
-          if (v) {
-            s = base + __ffs(v) - 1;
-            break;
-          }
-          from = 0;
-          base += 32;
-          if (base >= a.num_seqs) {
-            base = 0;
-            if ((int64_t)++rt * kRows >= (int64_t)a.max_query_len * a.group) {
-              left = 0;  // cannot happen while `left` counts tiles that exist
-              return false;
+    while (left > 0) {
+      if (at == tiles + kPieceCost) {
+        at = 0;
+        if (++kvh == a.num_kv_heads) {
+          kvh = 0;
+          int from = (s & 31) + 1;
+          while (true) {
+            const unsigned v = __ballot_sync(
+                0xffffffffu, (int)(threadIdx.x & 31) >= from &&
+                                 (int64_t)l_n * a.group > (int64_t)rt * kRows);
+            if (v) {
+              s = base + __ffs(v) - 1;
+              break;
             }
+            from = 0;
+            base += 32;
+            if (base >= a.num_seqs) {
+              base = 0;
+              if ((int64_t)++rt * kRows >= (int64_t)a.max_query_len * a.group) {
+                left = 0;  // cannot happen while `left` counts what exists
+                return false;
+              }
+            }
+            load(a);
           }
-          load(a);
+          tiles = tiles_of(__shfl_sync(0xffffffffu, l_ctx, s & 31));
         }
-        tiles = tiles_of(__shfl_sync(0xffffffffu, l_ctx, s & 31));
+      }
+      const int take = (int)min(left, (int64_t)(tiles + kPieceCost - at));
+      p.t0 = max(0, at - kPieceCost);
+      p.t1 = max(0, at + take - kPieceCost);
+      left -= take;
+      at += take;
+      if (p.t1 > p.t0) {
+        p.rt = rt;
+        p.s = s;
+        p.kvh = kvh;
+        p.tiles = tiles;
+        p.q0 = __shfl_sync(0xffffffffu, l_q0, s & 31);
+        p.n = __shfl_sync(0xffffffffu, l_n, s & 31);
+        p.ctx = __shfl_sync(0xffffffffu, l_ctx, s & 31);
+        return true;
       }
     }
-    p.rt = rt;
-    p.s = s;
-    p.kvh = kvh;
-    p.tiles = tiles;
-    p.q0 = __shfl_sync(0xffffffffu, l_q0, s & 31);
-    p.n = __shfl_sync(0xffffffffu, l_n, s & 31);
-    p.ctx = __shfl_sync(0xffffffffu, l_ctx, s & 31);
-    p.t0 = tile;
-    p.t1 = (int)min((int64_t)tiles, tile + left);
-    left -= p.t1 - p.t0;
-    tile = p.t1;
-    return true;
+    return false;
   }
 };
 
@@ -268,6 +299,91 @@ __device__ __forceinline__ uint64_t tile_view(const TreeArgs& a, int64_t row, in
   return v;
 }
 
+// Four E4M3 codes -> bf16 (exact). Sign, exponent and fraction move to their bf16 places, which
+// makes the value 2^-120 times too small; bf16 keeps subnormals, so one product restores
+// E4M3's as well. The two NaN codes come out as +-480: the caller looks for them.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+  lo = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+  hi = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+  const uint32_t up = 0x7b807b80u;  // 2^120, twice
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(up));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(up));
+}
+// Four int8 codes -> bf16 of code - zero (exact: at most 255 in size). The code + 128 becomes
+// the low byte of the float 2^23 + code + 128; z = 2^23 + 128 + zero.
+__device__ __forceinline__ void i8x4_to_bf16(uint32_t w, float z, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  float f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    f[e] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + e)) - z;
+  lo = pack_bf16x2(f[0], f[1]);
+  hi = pack_bf16x2(f[2], f[3]);
+}
+
+// The softmax of one tile for one row: S (64 columns of this lane in tensor memory at `sbuf`) to
+// P (bf16 pairs over its first 32 columns). Two passes of 32 columns each over S, which keeps
+// half the registers and code of one pass that holds all 64. `view`: keys the row sees (read
+// only when MASKED). Returns the factor that O and l have to be multiplied with.
+template <int BS, bool QUANT, bool MASKED>
+__device__ __forceinline__ float softmax_tile(uint32_t sbuf, const TileInfo& ti, float sl2,
+                                              uint64_t view, float& m_used, float& l) {
+  float m_new = m_used;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t sv[32];
+    tmem_ld32(sbuf + c * 32, sv);
+    tmem_wait_ld(sv);
+    const uint32_t v = MASKED ? (uint32_t)(view >> (32 * c)) : 0u;
+    float mx[4] = {m_new, m_new, m_new, m_new};
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float f = QUANT ? sl2 * ti.ks[c * (32 / BS) + e / BS] : sl2;
+      float z = __uint_as_float(sv[e]) * f;
+      if (MASKED && !((v >> e) & 1u)) z = -INFINITY;
+      mx[e & 3] = fmaxf(mx[e & 3], z);
+    }
+    m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  }
+  float alpha = 1.f;
+  if (m_new > m_used + 8.f) {  // lazy: P stays at or below 2^8 otherwise
+    alpha = fast_exp2(m_used - m_new);
+    m_used = m_new;
+  }
+  const float ref = m_used == -INFINITY ? 0.f : -m_used;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t sv[32], pk[16];
+    tmem_ld32(sbuf + c * 32, sv);
+    tmem_wait_ld(sv);
+    const uint32_t v = MASKED ? (uint32_t)(view >> (32 * c)) : 0u;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float f = QUANT ? sl2 * ti.ks[c * (32 / BS) + e / BS] : sl2;
+      float p0 = fast_exp2(fmaf(__uint_as_float(sv[e]), f, ref));
+      float p1 = fast_exp2(fmaf(__uint_as_float(sv[e + 1]), f, ref));
+      if (MASKED) {
+        p0 = ((v >> e) & 1u) ? p0 : 0.f;
+        p1 = ((v >> (e + 1)) & 1u) ? p1 : 0.f;
+      }
+      sum[e & 3] += p0;
+      sum[(e + 1) & 3] += p1;
+      if constexpr (QUANT) {  // P carries its block's V scale; a key that is not seen, none
+        const float vs = ti.vs[c * (32 / BS) + e / BS];
+        p0 = MASKED && p0 == 0.f ? 0.f : p0 * vs;
+        p1 = MASKED && p1 == 0.f ? 0.f : p1 * vs;
+      }
+      pk[e >> 1] = pack_bf16x2(p0, p1);
+    }
+    pf::tmem_st16(sbuf + c * 16, pk);  // over columns that both passes have read
+  }
+  l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+  tmem_wait_st();
+  return alpha;
+}
+
 template <int BS, pa_dtype KV>
 __global__ void __launch_bounds__(Layout<KV != PA_BF16>::kThreads, 2)
 tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUtensorMap qmap,
@@ -282,21 +398,23 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
                                              ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, TM = kRows / G, Hkv = a.num_kv_heads;
+  // a step of up to 64 rows per sequence keeps two pieces' Q (the product still reads 128
+  // rows: what lies behind the 64 gives rows that nobody uses)
+  const int q_rows = a.max_query_len * G <= kRows / 2 ? kRows / 2 : kRows;
+  const int q_bufs = kRows / q_rows;
   const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK);
   const uint32_t sV = smem_u32(smem + L::kOffV);
   const uint32_t bar0 = smem_u32(smem + L::kOffBar);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   TileInfo* info = reinterpret_cast<TileInfo*>(smem + L::kOffInfo);
-  int64_t* s_scan = reinterpret_cast<int64_t*>(smem + L::kOffMisc);          // [8]
-  int* s_start = reinterpret_cast<int*>(s_scan + 8);                        // rt, s, kvh, tile
+  int64_t* s_scan = reinterpret_cast<int64_t*>(smem + L::kOffMisc);          // [16]
+  int* s_start = reinterpret_cast<int*>(s_scan + 16);                       // rt, s, kvh, place
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_start + 4);
-  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // drafts of the current piece whose V row holds a NaN or infinity, by draft index
   // (two lists, for even and odd pieces: the converters may be one piece ahead)
   uint32_t* s_odd = reinterpret_cast<uint32_t*>(tmem_slot + 2);              // [2][8]
   volatile int* any_odd = reinterpret_cast<volatile int*>(s_odd + 16);       // [2]
 
-  pdl_wait();
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       uint32_t count = 1;
@@ -305,16 +423,16 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
                     (i >= L::kBarVF && i < L::kBarVF + L::kVSt) ||
                     (i >= L::kBarK8E && i < L::kBarK8E + L::kK8St) ||
                     (i >= L::kBarV8E && i < L::kBarV8E + L::kV8St)))
-        count = 32;  // one converter warp
+        count = 32 * kConvWarps;
       mbar_init(bar(i), count);
     }
-    *dead = 0;
     for (int i = 0; i < 16; ++i) s_odd[i] = 0;
     any_odd[0] = any_odd[1] = 0;
     s_start[0] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  pdl_wait();
   // ---- the batch's key tiles, and where this CTA's run begins ----
   const int rts = row_tiles_of(a.max_query_len, G);
   const int seqs_per = (a.num_seqs + kThreads - 1) / kThreads;
@@ -322,7 +440,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) {
     int q0, n, ctx;
-    if (seq_range(a, s, q0, n, ctx)) mine += (int64_t)row_tiles_of(n, G) * tiles_of(ctx);
+    if (seq_range(a, s, q0, n, ctx)) mine += (int64_t)row_tiles_of(n, G) * (tiles_of(ctx) + kPieceCost);
     else if (blockIdx.x == 0) flag_error(PA_DEVERR_QUERY);
   }
   int64_t total;
@@ -335,11 +453,12 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     return;
   }
   int64_t done = 0;
+#pragma unroll 1
   for (int rt = 0; rt < rts; ++rt) {
     int64_t sum = 0;
     for (int s = s0; s < s1; ++s) {
       int q0, n, ctx;
-      if (seq_range(a, s, q0, n, ctx) && row_tiles_of(n, G) > rt) sum += tiles_of(ctx);
+      if (seq_range(a, s, q0, n, ctx) && row_tiles_of(n, G) > rt) sum += tiles_of(ctx) + kPieceCost;
     }
     int64_t all;
     int64_t at = scan1<W>(sum, all, s_scan);
@@ -349,14 +468,14 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         for (int s = s0; s < s1; ++s) {
           int q0, n, ctx;
           if (!seq_range(a, s, q0, n, ctx) || row_tiles_of(n, G) <= rt) continue;
-          const int nt = tiles_of(ctx);
+          const int nt = tiles_of(ctx) + kPieceCost;
           if (w0 < at + (int64_t)nt * Hkv) {
             const int h = (int)((w0 - at) / nt);
             s_start[0] = rt;
             s_start[1] = s;
             s_start[2] = h;
             s_start[3] = (int)(w0 - at - (int64_t)h * nt);
-            ws.runs[blockIdx.x] = RunInfo{per, at + (int64_t)h * nt, rt, s, h, nt};
+            ws.runs[blockIdx.x] = RunInfo{per, at + (int64_t)h * nt, rt, s, h, tiles_of(ctx)};
             break;
           }
           at += (int64_t)nt * Hkv;
@@ -374,13 +493,12 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk walk;
-  walk.start(a, s_start[0] >= 0 ? count : 0, s_start[0], s_start[1], s_start[2], s_start[3]);
   // waits are made warp-uniform
   auto wait_all = [&](uint32_t b, uint32_t parity) {
-    const bool w = !*dead && mbar_wait(b, parity);
-    return __all_sync(0xffffffffu, w) != 0;
+    return __all_sync(0xffffffffu, mbar_wait(b, parity)) != 0;
   };
+  auto wait_info = [&](int g) { return wait_all(bar(L::kBarInfo + g % kInfo), (g / kInfo) & 1); };
+  bool ok = true;
 
   if (warp == kTmaWarp) {
     // ------------------------------ producer ------------------------------
@@ -390,87 +508,87 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       float ks, vs;
       int kz, vz;
       int tile0, ntiles; // its key tiles within the piece
-      int kvh, q_tok, ctx;
+      Piece pc;
       bool first, any;   // first of its piece; exists
     };
-    Piece pc;
-    bool have = walk.next(a, pc);
-    int wt = have ? pc.t0 : 0;
-    bool fresh = true;
-    auto next_window = [&](Window& w) {
-      w.any = have;
-      if (!have) return;
-      w.first = fresh;
-      w.tile0 = wt;
-      w.ntiles = min(WT, pc.t1 - wt);
-      w.kvh = pc.kvh;
-      w.q_tok = pc.q0 + pc.rt * TM;
-      w.ctx = pc.ctx;
-      w.p = -1;
-      w.ks = w.vs = 1.f;
-      w.kz = w.vz = 0;
-      const int blk = wt * NB + lane;
-      if (lane < w.ntiles * NB && blk * BS < pc.ctx) {
-        int p = a.block_tables[(int64_t)pc.s * a.max_blocks_per_seq + blk];
+    Walk walk;
+    walk.start(a, s_start[0] >= 0 ? count : 0, s_start[0], s_start[1], s_start[2], s_start[3]);
+    Window cur, nxt;
+    nxt.pc.t1 = 0;
+    int wt = 0;          // next tile of the piece in nxt
+    bool run_first = true;
+    nxt.any = true;
+    const uint64_t keep = tc::evict_first_policy();
+    int g = 0, pieces = 0;
+    // fetches the window behind the one in nxt (block ids and scales, used a window later)
+    auto next_window = [&]() {
+      if (!nxt.any) return;
+      nxt.first = wt == nxt.pc.t1;
+      if (nxt.first) {
+        nxt.any = walk.next(a, nxt.pc);
+        if (!nxt.any) return;
+        wt = nxt.pc.t0;
+      }
+      nxt.tile0 = wt;
+      nxt.ntiles = min(WT, nxt.pc.t1 - wt);
+      wt += nxt.ntiles;
+      nxt.p = -1;
+      nxt.ks = nxt.vs = 1.f;
+      nxt.kz = nxt.vz = 0;
+      const int blk = nxt.tile0 * NB + lane;
+      if (lane < nxt.ntiles * NB && blk * BS < nxt.pc.ctx) {
+        int p = a.block_tables[(int64_t)nxt.pc.s * a.max_blocks_per_seq + blk];
         if (p < 0 || p >= a.num_blocks) {
           flag_error(PA_DEVERR_BLOCK_ID);
           p = -1;
         } else if constexpr (QUANT) {
-          const int64_t bh = (int64_t)p * Hkv + pc.kvh;
-          w.ks = a.k_scales[bh];
-          w.vs = a.v_scales[bh];
+          const int64_t bh = (int64_t)p * Hkv + nxt.pc.kvh;
+          nxt.ks = a.k_scales[bh];
+          nxt.vs = a.v_scales[bh];
           if constexpr (KV == PA_INT8) {
-            w.kz = a.k_zeros[bh];
-            w.vz = a.v_zeros[bh];
-            if (!zero_in_range(w.kz) || !zero_in_range(w.vz)) {
+            nxt.kz = a.k_zeros[bh];
+            nxt.vz = a.v_zeros[bh];
+            if (!zero_in_range(nxt.kz) || !zero_in_range(nxt.vz)) {
               flag_error(PA_DEVERR_ZERO);
               p = -1;
             }
           }
         }
-        w.p = p;
-      }
-      wt += w.ntiles;
-      fresh = false;
-      if (wt == pc.t1) {
-        have = walk.next(a, pc);
-        wt = have ? pc.t0 : 0;
-        fresh = true;
+        nxt.p = p;
       }
     };
-    Window cur, nxt;
-    next_window(cur);
-    next_window(nxt);
-    const uint64_t keep = tc::evict_first_policy();
-    int g = 0, pieces = 0;
-    bool ok = true;
+    next_window();
+    cur = nxt;
+    next_window();
+#pragma unroll 1
     while (ok && cur.any) {
       if (cur.first) {
-        // the last S product of the piece before has read Q
-        if (pieces > 0) ok = wait_all(bar(L::kBarQE), (pieces - 1) & 1);
+        // the last S product of the piece that used this buffer has read it
+        const int qb = q_bufs == 2 ? pieces & 1 : 0, use = q_bufs == 2 ? pieces >> 1 : pieces;
+        if (use > 0) ok = wait_all(bar(L::kBarQE + qb), (use - 1) & 1);
         if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_tx(bar(L::kBarQF), kQBytes);
-#pragma unroll
+          const int slab = q_rows * 128;
+          mbar_arrive_tx(bar(L::kBarQF + qb), 2 * slab);
+#pragma unroll 1
           for (int h = 0; h < 2; ++h)
-            pf::tma_load_4d(sQ + h * kQSlab, &qmap, 0, h, cur.kvh * G, cur.q_tok, bar(L::kBarQF),
-                            keep);
+            pf::tma_load_4d(sQ + (2 * qb + h) * slab, &qmap, 0, h, cur.pc.kvh * G,
+                            cur.pc.q0 + cur.pc.rt * TM, bar(L::kBarQF + qb), keep);
         }
         __syncwarp();
         ++pieces;
       }
+#pragma unroll 1
       for (int k = 0; k < cur.ntiles; ++k, ++g) {
         // this tile's blocks sit in lanes k * NB ..
-        const int src = (k * NB + (lane & (NB - 1))) & 31;
+        const int src = (k * NB + (lane & (NB - 1))) & 31, tile = cur.tile0 + k;
         const int p = __shfl_sync(0xffffffffu, cur.p, src);
-        const bool exists = (cur.tile0 + k) * kKeys + (lane & (NB - 1)) * BS < cur.ctx;
+        const bool exists = tile * kKeys + (lane & (NB - 1)) * BS < cur.pc.ctx;
         const uint32_t good = __ballot_sync(0xffffffffu, lane < NB && p >= 0);
         const uint32_t bad = __ballot_sync(0xffffffffu, lane < NB && p < 0 && exists);
-        const float ks = __shfl_sync(0xffffffffu, cur.ks, src), vs = __shfl_sync(0xffffffffu, cur.vs, src);
-        const int kz = __shfl_sync(0xffffffffu, cur.kz, src), vz = __shfl_sync(0xffffffffu, cur.vz, src);
         const int pb = __shfl_sync(0xffffffffu, p, (lane >> 1) & (NB - 1));
         // ---- K, then V: the ring's stage is free once its last reader is done ----
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           const int nst = QUANT ? (kv ? L::kV8St : L::kK8St) : (kv ? L::kVSt : L::kKSt);
           const int full = QUANT ? (kv ? L::kBarV8F : L::kBarK8F) : (kv ? L::kBarVF : L::kBarKF);
@@ -483,12 +601,36 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
             // could only be read after S(g - 4) at the earliest, which was issued behind
             // P V (g - 6), so softmax and converters are past tile g - 6 > g - kInfo.
             TileInfo& ti = info[g % kInfo];
-            if (lane == 0) ti.bad = bad;
-            if (QUANT && lane < NB) {
-              ti.ks[lane] = ks;
-              ti.vs[lane] = vs;
-              ti.kz[lane] = kz;
-              ti.vz[lane] = vz;
+            if (lane == 0) {
+              const Piece& pc = cur.pc;
+              const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
+              ti.flags = (tile == pc.t0 ? kFirst : 0) | (tile == pc.t1 - 1 ? kLast : 0) |
+                         (whole ? kWhole : 0);
+              ti.bad = bad;
+              ti.key0 = tile * kKeys;
+              ti.base = pc.ctx - pc.n;
+              ti.ctx = pc.ctx;
+              ti.row0 = pc.q0 + pc.rt * TM;
+              ti.rows = min(TM, pc.n - pc.rt * TM);
+              ti.s = pc.s;
+              ti.kvh = pc.kvh;
+              ti.slot = blockIdx.x * 2 + (run_first ? 0 : 1);
+            }
+            if constexpr (QUANT) {
+              const float ks = __shfl_sync(0xffffffffu, cur.ks, src);
+              const float vs = __shfl_sync(0xffffffffu, cur.vs, src);
+              if (lane < NB) {
+                ti.ks[lane] = ks;
+                ti.vs[lane] = vs;
+              }
+              if constexpr (KV == PA_INT8) {
+                const int kz = __shfl_sync(0xffffffffu, cur.kz, src);
+                const int vz = __shfl_sync(0xffffffffu, cur.vz, src);
+                if (lane < NB) {
+                  ti.kz[lane] = kz;
+                  ti.vz[lane] = vz;
+                }
+              }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::kBarInfo + g % kInfo));
@@ -501,29 +643,30 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
             if (lane < NB && p >= 0)
               tc::tma_load_2d(smem_u32(smem + (kv ? L::kOffV8 : L::kOffK8)) + st * kCodeBytes +
                                   lane * BS * 128,
-                              kv ? &vmap : &kmap, 0, (p * Hkv + cur.kvh) * BS, fb, keep);
+                              kv ? &vmap : &kmap, 0, (p * Hkv + cur.pc.kvh) * BS, fb, keep);
           } else {
             if (lane < 2 * NB && pb >= 0)
               pf::tma_load_3d((kv ? sV : sK) + st * kKVBytes + (lane & 1) * kKVSlab +
                                   (lane >> 1) * BS * 128,
-                              kv ? &vmap : &kmap, 0, lane & 1, (pb * Hkv + cur.kvh) * BS, fb);
+                              kv ? &vmap : &kmap, 0, lane & 1, (pb * Hkv + cur.pc.kvh) * BS, fb);
           }
         }
         if (!ok) break;
       }
       if (!ok) break;
+      if (cur.tile0 + cur.ntiles == cur.pc.t1) run_first = false;
       cur = nxt;
-      next_window(nxt);
+      next_window();
     }
-    if (!ok) {
-      if (lane == 0) {
-        flag_error(PA_DEVERR_TIMEOUT);
-        *dead = 1;
-      }
-      __syncwarp();
-      // copies in flight complete (each barrier's last phase) before shared memory is released
-      if (lane == 0) {
-        if (pieces > 0) mbar_wait(bar(L::kBarQF), (pieces - 1) & 1);
+    if (lane == 0) {
+      if (ok) {  // the slot is free as above
+        info[g % kInfo].flags = kEnd;
+        mbar_arrive(bar(L::kBarInfo + g % kInfo));
+      } else {
+        // copies in flight complete (each barrier's last phase) before shared memory is released
+        for (int i = max(0, pieces - q_bufs); i < pieces; ++i)
+          mbar_wait(bar(L::kBarQF + i % q_bufs), (i / q_bufs) & 1);
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           const int nst = QUANT ? (kv ? L::kV8St : L::kK8St) : (kv ? L::kVSt : L::kKSt);
           const int full = QUANT ? (kv ? L::kBarV8F : L::kBarK8F) : (kv ? L::kBarVF : L::kBarKF);
@@ -535,71 +678,68 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------ MMA issuer ------------------------------
-    Piece pc;
-    auto issue_s = [&](int g) {
-      const uint32_t kst = sK + (g % L::kKSt) * kKVBytes;
-#pragma unroll
-      for (int kk = 0; kk < kDim / 16; ++kk)
-        pf::umma_bf16(tmem + (g & 1) * kKeys,
-                      sdesc(sQ + (kk >> 2) * kQSlab + (kk & 3) * 32, 16, 1024),
-                      sdesc(kst + (kk >> 2) * kKVSlab + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0);
-      umma_commit(bar(L::kBarSF + (g & 1)));
-      umma_commit(bar(L::kBarKE + g % L::kKSt));
-    };
-    auto issue_pv = [&](int g, bool fresh) {
-      const uint32_t vst = sV + (g % L::kVSt) * kKVBytes;
-#pragma unroll
-      for (int kk = 0; kk < kKeys / 16; ++kk)
-        pf::umma_bf16_ts(tmem + kOCol, tmem + (g & 1) * kKeys + kk * 8,
-                         sdesc(vst + kk * 16 * 128, kKVSlab, 1024), kIdescPV, !fresh || kk > 0);
-      umma_commit(bar(L::kBarO + (g & 1)));
-      umma_commit(bar(L::kBarVE + g % L::kVSt));
-    };
-    int g = 0, pieces = 0;      // tiles whose S is issued; pieces whose Q is in use
-    int left = 0;               // tiles of the current piece whose S is not issued
-    bool ok = true, fresh_s = false;
-    bool fresh_pv[2] = {true, true};
-    // S of the next tile of the run; false when there is none (or a wait gave up)
+    int g = 0, pieces = 0, q_buf = 0;   // tiles whose S is issued; pieces whose Q is in use
+    uint32_t q_at = sQ;
+    uint32_t fresh = 0;                 // bit b: P V from S buffer b begins a piece
+    // S of the run's next tile; false when there is none (or a wait gave up)
     auto next_s = [&]() {
-      if (left == 0) {
-        if (!walk.next(a, pc)) return false;
-        left = pc.t1 - pc.t0;
-        fresh_s = true;
-        ok = wait_all(bar(L::kBarQF), pieces & 1);
+      ok = wait_info(g);
+      if (!ok) return false;
+      const int flags = info[g % kInfo].flags;
+      if (flags & kEnd) return false;
+      if (flags & kFirst) {
+        q_buf = q_bufs == 2 ? pieces & 1 : 0;
+        ok = wait_all(bar(L::kBarQF + q_buf), (q_bufs == 2 ? pieces >> 1 : pieces) & 1);
         if (!ok) return false;
+        q_at = sQ + q_buf * q_rows * 256;
         ++pieces;
       }
       ok = wait_all(bar(L::kBarKF + g % L::kKSt), (g / L::kKSt) & 1);
       if (!ok) return false;
       tc_fence_after();
-      fresh_pv[g & 1] = fresh_s;
-      fresh_s = false;
-      --left;
+      const uint32_t b = 1u << (g & 1);
+      fresh = (flags & kFirst) ? fresh | b : fresh & ~b;
       if (lane == 0) {
-        issue_s(g);
-        if (left == 0) umma_commit(bar(L::kBarQE));
+        const uint32_t kst = sK + (g % L::kKSt) * kKVBytes;
+#pragma unroll
+        for (int kk = 0; kk < kDim / 16; ++kk)
+          pf::umma_bf16(tmem + (g & 1) * kKeys,
+                        sdesc(q_at + (kk >> 2) * q_rows * 128 + (kk & 3) * 32, 16, 1024),
+                        sdesc(kst + (kk >> 2) * kKVSlab + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0);
+        umma_commit(bar(L::kBarSF + (g & 1)));
+        umma_commit(bar(L::kBarKE + g % L::kKSt));
+        if (flags & kLast) umma_commit(bar(L::kBarQE + q_buf));
       }
       __syncwarp();
       ++g;
       return true;
     };
-    bool more = next_s();
-    for (int j = 0; ok && more; ++j) {
-      more = next_s();
+#pragma unroll 1
+    for (int j = -1; ok; ++j) {
+      const bool more = next_s();
       if (!ok) break;
+      if (j < 0) {
+        if (!more) break;
+        continue;
+      }
       ok = wait_all(bar(L::kBarP + (j & 1)), (j >> 1) & 1) &&
            wait_all(bar(L::kBarVF + j % L::kVSt), (j / L::kVSt) & 1);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) issue_pv(j, fresh_pv[j & 1]);
+      if (lane == 0) {
+        const uint32_t vst = sV + (j % L::kVSt) * kKVBytes;
+        const bool acc = !((fresh >> (j & 1)) & 1u);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          pf::umma_bf16_ts(tmem + kOCol, tmem + (j & 1) * kKeys + kk * 8,
+                           sdesc(vst + kk * 16 * 128, kKVSlab, 1024), kIdescPV, acc || kk > 0);
+        umma_commit(bar(L::kBarO + (j & 1)));
+        umma_commit(bar(L::kBarVE + j % L::kVSt));
+      }
       __syncwarp();
-      more = j + 1 < g;
+      if (j + 1 == g) break;  // no tile behind this one
     }
     if (lane == 0) {
-      if (!ok) {
-        flag_error(PA_DEVERR_TIMEOUT);
-        *dead = 1;
-      }
       // every product of the CTA completes before tensor memory is released
       umma_commit(bar(L::kBarFin));
       mbar_wait(bar(L::kBarFin), 0);
@@ -607,89 +747,80 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     __syncwarp();
   } else if (QUANT && warp >= kConvWarp) {
     // ------------------------------ converters ------------------------------
-    // Warp 6 turns K tiles, warp 7 V tiles. A lane takes 16 codes at a time: value = the E4M3
-    // code's value or code - zero, exact in bf16, stored where TMA would put bf16 (128-byte
-    // rows of 64 channels, 16-byte chunks XORed with row % 8). V rows that cannot be read or
-    // lie behind the context become zero, and so do NaN codes of drafts: P is zero for rows
-    // that do not see them, but 0 * NaN is not (rows that see one get it back at the end).
-    const int kv = warp - kConvWarp;
+    // The first kConvWarps warps turn K tiles, the others V tiles, sharing a tile's rows. A lane
+    // takes 16 codes at a time: value = the E4M3 code's value or code - zero, exact in bf16,
+    // stored where TMA would put bf16 (128-byte rows of 64 channels, 16-byte chunks XORed with
+    // row % 8). V rows that cannot be read or lie behind the context become zero, and so do
+    // NaN codes of drafts: P is zero for rows that do not see them, but 0 * NaN is not (rows
+    // that see one get it back at the end).
+    const int kv = (warp - kConvWarp) / kConvWarps, sub = (warp - kConvWarp) % kConvWarps;
     const int nst = kv ? L::kVSt : L::kKSt, nst8 = kv ? L::kV8St : L::kK8St;
-    Piece pc;
-    int g = 0, par = 1;
-    bool ok = true;
-    while (ok && walk.next(a, pc)) {
-      par ^= 1;
-      for (int t = pc.t0; t < pc.t1 && ok; ++t, ++g) {
-        const int st = g % nst, st8 = g % nst8;
-        ok = wait_all(bar(L::kBarInfo + g % kInfo), (g / kInfo) & 1) &&
-             wait_all(bar((kv ? L::kBarV8F : L::kBarK8F) + st8), (g / nst8) & 1);
-        if (ok && g >= nst)
-          ok = wait_all(bar((kv ? L::kBarVE : L::kBarKE) + st), ((g / nst) - 1) & 1);
-        if (!ok) break;
-        const TileInfo& ti = info[g % kInfo];
-        const uint8_t* src = smem + (kv ? L::kOffV8 + st8 * kCodeBytes : L::kOffK8 + st8 * kCodeBytes);
-        const uint32_t dst = (kv ? sV : sK) + st * kKVBytes;
-        const int live = pc.ctx - t * kKeys, base = pc.ctx - pc.n;
-        const uint32_t bad = ti.bad;
-#pragma unroll 4
-        for (int it = 0; it < kKeys * 8 / 32; ++it) {
-          const int key = it * 4 + (lane >> 3), q8 = lane & 7;
-          const uint4 raw = *reinterpret_cast<const uint4*>(src + key * 128 + q8 * 16);
-          const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
-          uint32_t o[8];
-          const float z = KV == PA_INT8 ? (float)(kv ? ti.vz[key / BS] : ti.kz[key / BS]) : 0.f;
+    int par = 1;
+#pragma unroll 1
+    for (int g = 0;; ++g) {
+      const int st = g % nst, st8 = g % nst8;
+      ok = wait_info(g);
+      if (!ok) break;
+      const TileInfo& ti = info[g % kInfo];
+      const int flags = ti.flags;
+      if (flags & kEnd) break;
+      if (flags & kFirst) par ^= 1;
+      ok = wait_all(bar((kv ? L::kBarV8F : L::kBarK8F) + st8), (g / nst8) & 1);
+      if (ok && g >= nst) ok = wait_all(bar((kv ? L::kBarVE : L::kBarKE) + st), ((g / nst) - 1) & 1);
+      if (!ok) break;
+      const uint8_t* src = smem + (kv ? L::kOffV8 : L::kOffK8) + st8 * kCodeBytes;
+      const uint32_t dst = (kv ? sV : sK) + st * kKVBytes;
+      const int live = ti.ctx - ti.key0, draft0 = ti.base - ti.key0;
+      const uint32_t bad = ti.bad;
+      const int q8 = lane & 7, c0 = 2 * (q8 & 3);
+#pragma unroll 2
+      for (int it = sub; it < kKeys * 8 / 32; it += kConvWarps) {
+        const int key = it * 4 + (lane >> 3);
+        const uint4 raw = *reinterpret_cast<const uint4*>(src + key * 128 + q8 * 16);
+        const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
+        const uint32_t row = dst + (q8 >> 2) * kKVSlab + key * 128;
+        uint32_t o[8];
+        uint32_t nan = 0;
+        const bool gone = kv && (key >= live || ((bad >> (key / BS)) & 1u));
+        if constexpr (KV == PA_INT8) {
+          const float z = 8388736.f + (float)(kv ? ti.vz[key / BS] : ti.kz[key / BS]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) i8x4_to_bf16(wd[k], z, o[2 * k], o[2 * k + 1]);
+        } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float f[4];
-            if constexpr (KV == PA_INT8) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(wd[k] >> (8 * e)) - z;
-            } else {
-              pf::f16x2_to_f32(e4m3x2_to_f16x2((uint16_t)(wd[k] & 0xffffu)), f[0], f[1]);
-              pf::f16x2_to_f32(e4m3x2_to_f16x2((uint16_t)(wd[k] >> 16)), f[2], f[3]);
-            }
-            o[2 * k] = pack_bf16x2(f[0], f[1]);
-            o[2 * k + 1] = pack_bf16x2(f[2], f[3]);
+            nan |= ((wd[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            e4m3x4_to_bf16(wd[k], o[2 * k], o[2 * k + 1]);
           }
-          if (kv) {
-            const bool gone = key >= live || ((bad >> (key / BS)) & 1u);
-            if (gone) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = 0;
-            } else if (KV == PA_FP8_E4M3 && t * kKeys + key >= base) {
-              bool odd = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (((wd[k] >> (8 * e)) & 0x7fu) == 0x7fu) {
-                    odd = true;
-                    o[2 * k + (e >> 1)] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
-                  }
-              if (odd) {
-                const int j = t * kKeys + key - base;
-                atomicOr(&s_odd[par * 8 + (j >> 5)], 1u << (j & 31));
-                any_odd[par] = 1;
-              }
-            }
-          }
-          const uint32_t row = dst + (q8 >> 2) * kKVSlab + key * 128;
-          const int c0 = 2 * (q8 & 3);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                       ::"r"(row + ((c0 ^ (key & 7)) << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
-                         "r"(o[3]) : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                       ::"r"(row + (((c0 + 1) ^ (key & 7)) << 4)), "r"(o[4]), "r"(o[5]),
-                         "r"(o[6]), "r"(o[7]) : "memory");
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(bar((kv ? L::kBarV8E : L::kBarK8E) + st8));
-        mbar_arrive(bar((kv ? L::kBarVF : L::kBarKF) + st));
+        if (gone) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = 0;
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     ::"r"(row + ((c0 ^ (key & 7)) << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                       "r"(o[3]) : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     ::"r"(row + (((c0 + 1) ^ (key & 7)) << 4)), "r"(o[4]), "r"(o[5]),
+                       "r"(o[6]), "r"(o[7]) : "memory");
+        if (KV == PA_FP8_E4M3 && nan != 0 && !gone) {
+          const bool draft = kv && key >= draft0;
+#pragma unroll 1
+          for (int e = 0; e < 16; ++e)
+            if ((src[key * 128 + q8 * 16 + e] & 0x7f) == 0x7f)
+              asm volatile("st.shared.b16 [%0], %1;"
+                           ::"r"(row + (((c0 + (e >> 3)) ^ (key & 7)) << 4) + (e & 7) * 2),
+                             "h"((uint16_t)(draft ? 0 : 0x7fc0)) : "memory");
+          if (draft) {
+            const int j = key - draft0;
+            atomicOr(&s_odd[par * 8 + (j >> 5)], 1u << (j & 31));
+            any_odd[par] = 1;
+          }
+        }
       }
-    }
-    if (!ok && lane == 0) {
-      flag_error(PA_DEVERR_TIMEOUT);
-      *dead = 1;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(bar((kv ? L::kBarV8E : L::kBarK8E) + st8));
+      mbar_arrive(bar((kv ? L::kBarVF : L::kBarKF) + st));
     }
   } else if (warp < 4) {
     // ------------------------------ softmax ------------------------------
@@ -697,160 +828,126 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     const int tok = r / G, head = r - tok * G;
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
     const float sl2 = a.scale_log2;
-    Piece pc;
-    int g = 0;
-    bool ok = true;
-    bool first_piece = true;
     int par = 1;
     uint32_t syncs = 0;
+    float m_used = -INFINITY, l = 0.f;
     // the four warps meet, within a bound (one of them may have given up)
     auto meet = [&]() {
       mbar_arrive(bar(L::kBarSm));
       return wait_all(bar(L::kBarSm), syncs++ & 1);
     };
-    while (ok && walk.next(a, pc)) {
-      par ^= 1;
-      const int rows = min(TM, pc.n - pc.rt * TM);     // tokens of the tile
-      const bool live_row = tok < rows;
-      const bool live_warp = warp * 32 < rows * G;
-      const int64_t row = pc.q0 + pc.rt * TM + min(tok, rows - 1);
-      const int base = pc.ctx - pc.n;
-      float m_used = -INFINITY, l = 0.f;
-      for (int t = pc.t0; t < pc.t1; ++t, ++g) {
-        const int t0 = t * kKeys, live = pc.ctx - t0;
+#pragma unroll 1
+    for (int g = 0;; ++g) {
+      ok = wait_info(g);
+      if (!ok) break;
+      const TileInfo& ti = info[g % kInfo];
+      const int flags = ti.flags;
+      if (flags & kEnd) break;
+      if (flags & kFirst) {
+        m_used = -INFINITY;
+        l = 0.f;
+        par ^= 1;
+      }
+      const bool live_warp = warp * 32 < ti.rows * G;
+      const int64_t row = ti.row0 + min(tok, ti.rows - 1);
+      const uint32_t bad = ti.bad;
+      const int base = ti.base, live = ti.ctx - ti.key0, draft0 = base - ti.key0;
+      const bool masked = draft0 < kKeys || bad != 0;
+      uint64_t view = ~0ull;
+      if (masked && live_warp) {
+        view = tile_view(a, row, ti.key0, base, ti.ctx);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          if ((bad >> b) & 1u) view &= ~(((1ull << BS) - 1ull) << (b * BS));
+      }
+      ok = wait_all(bar(L::kBarSF + (g & 1)), (g >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (live_warp) {
         const uint32_t sbuf = lanes + (g & 1) * kKeys;
-        ok = wait_all(bar(L::kBarInfo + g % kInfo), (g / kInfo) & 1) &&
-             wait_all(bar(L::kBarSF + (g & 1)), (g >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const TileInfo& ti = info[g % kInfo];
-        const uint32_t bad = ti.bad;
-        if (live_warp) {
-          uint32_t sv[2][32];
-          tmem_ld32(sbuf, sv[0]);
-          tmem_ld32(sbuf + 32, sv[1]);
-          tmem_wait_ld(sv[0]);
-          tmem_wait_ld(sv[1]);
-          // scores in the log2 domain (with the K scale of their block), then the mask
+        const float alpha =
+            masked ? softmax_tile<BS, QUANT, true>(sbuf, ti, sl2, view, m_used, l)
+                   : softmax_tile<BS, QUANT, false>(sbuf, ti, sl2, view, m_used, l);
+        if (!(flags & kFirst) && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O holds the tiles before this one once their last product is done
+          ok = wait_all(bar(L::kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(lanes + kOCol + c * 32, o);
+            tmem_wait_ld(o);
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float f = QUANT ? sl2 * ti.ks[(c * 32 + e) / BS] : sl2;
-              sv[c][e] = __float_as_uint(__uint_as_float(sv[c][e]) * f);
-            }
-          if (t0 + kKeys > base || bad != 0) {
-            uint64_t v = tile_view(a, row, t0, base, pc.ctx);
-            if (bad != 0) {
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-                if ((bad >> b) & 1u) v &= ~(((1ull << BS) - 1ull) << (b * BS));
-            }
-            const uint32_t v2[2] = {(uint32_t)v, (uint32_t)(v >> 32)};
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((v2[c] >> e) & 1u)) sv[c][e] = 0xff800000u;  // -inf
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(lanes + kOCol + c * 32, o);
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[c][e]));
-          const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          float alpha = 1.f;
-          if (m_new > m_used + 8.f) {  // lazy: P stays at or below 2^8 otherwise
-            alpha = fast_exp2(m_used - m_new);
-            m_used = m_new;
-          }
-          const float mref = m_used == -INFINITY ? 0.f : m_used;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0 = fast_exp2(__uint_as_float(sv[c][e]) - mref);
-              float p1 = fast_exp2(__uint_as_float(sv[c][e + 1]) - mref);
-              sum[e & 3] += p0;
-              sum[(e + 1) & 3] += p1;
-              if constexpr (QUANT) {  // P carries the V scale; a masked key carries none
-                const float vs = ti.vs[(c * 32 + e) / BS];
-                p0 = p0 == 0.f ? 0.f : p0 * vs;
-                p1 = p1 == 0.f ? 0.f : p1 * vs;
-              }
-              pk[c * 16 + (e >> 1)] = pack_bf16x2(p0, p1);
-            }
-          tmem_st32(sbuf, pk);
-          l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
           tmem_wait_st();
-          if (t > pc.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // O holds the tiles before this one once their last product is done
-            ok = wait_all(bar(L::kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32(lanes + kOCol + c * 32, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(lanes + kOCol + c * 32, o);
-            }
-            tmem_wait_st();
-          }
         }
-        if constexpr (!QUANT) {
-          // V rows that cannot be read or lie behind the context may hold anything: zero
-          // them. A NaN or infinity in a draft's V row is taken out too (see the converters).
-          if (live < kKeys || bad != 0 || t0 + kKeys > base) {
-            ok = wait_all(bar(L::kBarVF + g % L::kVSt), (g / L::kVSt) & 1);
-            if (!ok) break;
-            const int key = r & (kKeys - 1);
-            const uint32_t vrow = sV + (g % L::kVSt) * kKVBytes + (r >> 6) * kKVSlab + key * 128;
-            if (key >= live || ((bad >> (key / BS)) & 1u)) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + k * 16), "r"(0)
-                             : "memory");
-            } else if (t0 + key >= base) {
+      }
+      if constexpr (!QUANT) {
+        // V rows that cannot be read or lie behind the context may hold anything: zero them.
+        // A NaN or infinity in a draft's V row is taken out too (see the converters).
+        if (masked || live < kKeys) {
+          ok = wait_all(bar(L::kBarVF + g % L::kVSt), (g / L::kVSt) & 1);
+          if (!ok) break;
+          const int key = r & (kKeys - 1);
+          const uint32_t vrow = sV + (g % L::kVSt) * kKVBytes + (r >> 6) * kKVSlab + key * 128;
+          const bool gone = key >= live || ((bad >> (key / BS)) & 1u);
+          if (gone || key >= draft0) {
 #pragma unroll 1
-              for (int k = 0; k < 32; ++k) {
-                const uint32_t addr = vrow + ((k + r) & 31) * 4;
-                uint32_t x;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
-                const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
-                if (lo || hi) {
-                  x &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
-                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-                  const int j = t0 + key - base;
-                  atomicOr(&s_odd[par * 8 + (j >> 5)], 1u << (j & 31));
-                  any_odd[par] = 1;
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t addr = vrow + ((k + r) & 7) * 16;
+              uint32_t x[4] = {0, 0, 0, 0};
+              bool odd = false;
+              if (!gone) {
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const bool lo = (x[i] & 0x7f80u) == 0x7f80u, hi = (x[i] & 0x7f800000u) == 0x7f800000u;
+                  odd |= lo || hi;
+                  x[i] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
                 }
               }
+              if (gone || odd)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                             ::"r"(addr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+              if (odd) {
+                const int j = key - draft0;
+                atomicOr(&s_odd[par * 8 + (j >> 5)], 1u << (j & 31));
+                any_odd[par] = 1;
+              }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        tc_fence_before();
-        mbar_arrive(bar(L::kBarP + (g & 1)));
       }
-      if (!ok) break;
+      tc_fence_before();
+      mbar_arrive(bar(L::kBarP + (g & 1)));
+      if (!(flags & kLast)) continue;
+
       // ---- the piece is done: O / l, or the partial ----
-      ok = wait_all(bar(L::kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
+      // what the slot says is read before the slot can be reused (the wait below ends after
+      // this tile's product, several tiles before that)
+      const int rows = ti.rows, kvh = ti.kvh, seq = ti.s, ctx = ti.ctx;
+      const int64_t slot = ti.slot;
+      const bool has_drafts = ti.key0 + kKeys > base;
+      const bool live_row = tok < rows, whole = (flags & kWhole) != 0;
+      ok = wait_all(bar(L::kBarO + (g & 1)), (g >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
       // rows that see a draft with a NaN or infinity in V get it back: the four warps have
       // all written the list before one reads it, and read it before it is emptied
-      ok = meet();
-      if (!ok) break;
-      const bool odd = any_odd[par] != 0;
-      const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
-      const int64_t slot = (int64_t)blockIdx.x * 2 + (first_piece ? 0 : 1);
-      const int64_t orow = row * a.num_q_heads + pc.kvh * G + head;
+      bool odd = false;
+      if (KV != PA_INT8 && has_drafts) {
+        ok = meet();
+        if (!ok) break;
+        odd = any_odd[par] != 0;
+      }
+      const int64_t orow = row * a.num_q_heads + kvh * G + head;
+      uint16_t* op = static_cast<uint16_t*>(a.out) + orow * kDim;
+      float4* ap = reinterpret_cast<float4*>(ws.acc) + slot * (kDim / 4) * kRows + r;
       const float inv = l != 0.f ? 1.f / l : 0.f;
       if (live_warp) {
 #pragma unroll 1
@@ -858,29 +955,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
           uint32_t o[32];
           tmem_ld32(lanes + kOCol + c * 32, o);
           tmem_wait_ld(o);
-          if (odd && live_row) {
-            for (int j = 0; j < pc.n; ++j) {
-              if (!((s_odd[par * 8 + (j >> 5)] >> (j & 31)) & 1u)) continue;
-              if (!((a.tree_mask[row * a.mask_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
-              const int key = base + j;
-              const int64_t blk = a.block_tables[(int64_t)pc.s * a.max_blocks_per_seq + key / BS];
-              const int64_t at = ((blk * Hkv + pc.kvh) * BS + key % BS) * kDim + c * 32;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float v = 0.f;
-                if constexpr (!QUANT) {
-                  v = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.v_cache)[at + e] << 16);
-                  if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) v = 0.f;
-                } else {
-                  if ((static_cast<const uint8_t*>(a.v_cache)[at + e] & 0x7f) == 0x7f)
-                    v = __uint_as_float(0x7fc00000u);
-                }
-                o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
-              }
-            }
-          }
           if (live_row && whole) {
-            uint16_t* op = static_cast<uint16_t*>(a.out) + orow * kDim + c * 32;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint4 w;
@@ -888,14 +963,14 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
               w.y = pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv);
               w.z = pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv);
               w.w = pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv);
-              *reinterpret_cast<uint4*>(op + 8 * k) = w;
+              *reinterpret_cast<uint4*>(op + c * 32 + 8 * k) = w;
             }
           } else if (live_row) {
-            float4* ap = reinterpret_cast<float4*>(ws.acc) + (slot * (kDim / 4) + c * 8) * kRows + r;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              ap[k * kRows] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                          __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+              ap[(c * 8 + k) * kRows] =
+                  make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                              __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
           }
           __syncwarp();
         }
@@ -909,7 +984,34 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
           }
         }
       }
-      if (odd) {
+      if (odd) {  // rare: what this thread wrote is mended in place
+        if (live_row) {
+#pragma unroll 1
+          for (int j = 0; j < ctx - base; ++j) {
+            if (!((s_odd[par * 8 + (j >> 5)] >> (j & 31)) & 1u)) continue;
+            if (!((a.tree_mask[row * a.mask_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
+            const int key = base + j;
+            const int64_t blk = a.block_tables[(int64_t)seq * a.max_blocks_per_seq + key / BS];
+            const int64_t at = ((blk * Hkv + kvh) * BS + key % BS) * kDim;
+#pragma unroll 1
+            for (int d = 0; d < kDim; ++d) {
+              float v;
+              if constexpr (!QUANT) {
+                v = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.v_cache)[at + d] << 16);
+                if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) continue;
+              } else {
+                if ((static_cast<const uint8_t*>(a.v_cache)[at + d] & 0x7f) != 0x7f) continue;
+                v = __uint_as_float(0x7fc00000u);
+              }
+              if (whole) {
+                const float x = __uint_as_float((uint32_t)op[d] << 16) + v;
+                op[d] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffff);
+              } else {
+                reinterpret_cast<float*>(ap + (d >> 2) * kRows)[d & 3] += v;
+              }
+            }
+          }
+        }
         ok = meet();
         if (!ok) break;
         if (tid < 8) s_odd[par * 8 + tid] = 0;
@@ -918,13 +1020,9 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         if (!ok) break;
       }
       tc_fence_before();  // O is read before the next P is handed over
-      first_piece = false;
-    }
-    if (!ok && lane == 0) {
-      flag_error(PA_DEVERR_TIMEOUT);
-      *dead = 1;
     }
   }
+  if (!ok && lane == 0) flag_error(PA_DEVERR_TIMEOUT);
 
   // ------------------------------ teardown ------------------------------
   tc_fence_before();
@@ -945,17 +1043,18 @@ __global__ void __launch_bounds__(128) tree_tc_reduce_kernel(const TreeArgs a, c
   pdl_trigger();
   const int b = blockIdx.x + 1;
   const RunInfo run = ws.runs[b];
-  if (run.tiles == 0 || run.begin == run.per * b) return;    // no run, or cut between two
-  const int first = (int)(run.begin / run.per);
+  const int64_t tile0 = run.begin + kPieceCost;               // where its first tile is
+  if (run.tiles == 0 || run.per * b <= tile0) return;         // no run, or no tile cut off
+  const int first = (int)(tile0 / run.per);
   if (first != b - 1) return;
-  const int last = (int)((run.begin + run.tiles - 1) / run.per);
+  const int last = (int)((tile0 + run.tiles - 1) / run.per);
   const int G = a.group, TM = kRows / G;
   const int q0 = a.query_start[run.s], n = a.query_start[run.s + 1] - q0;
   const int rows = min(TM, n - run.rt * TM) * G;
   const int r = 32 * blockIdx.y + (threadIdx.x & 31), w = threadIdx.x >> 5;
   if (r >= rows) return;
   auto slot_of = [&](int k) {
-    return (int64_t)k * 2 + (k == first && run.begin != run.per * first ? 1 : 0);
+    return (int64_t)k * 2 + (k == first && run.begin > run.per * first ? 1 : 0);
   };
   float M = -INFINITY;
 #pragma unroll 4
@@ -993,6 +1092,21 @@ __global__ void __launch_bounds__(128) tree_tc_reduce_kernel(const TreeArgs a, c
     a.lse_out[row] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
+// q [T][Hq][128] as (64 channels, half, head, token); a box is the Q tile's rows of one half.
+inline bool make_q_map(CUtensorMap* m, const TreeArgs& a) {
+  auto enc = tc::encoder();
+  if (enc == nullptr) return false;
+  const int rows = a.max_query_len * a.group <= kRows / 2 ? kRows / 2 : kRows;
+  cuuint64_t dims[4] = {64, 2, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.num_tokens};
+  cuuint64_t strides[3] = {128, 256, (cuuint64_t)a.num_q_heads * 256};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)a.group, (cuuint32_t)(rows / a.group)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.q), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
 template <int BS, pa_dtype KV>
 inline cudaError_t launch_bs(const TreeArgs& a, const Workspace& ws, cudaStream_t st) {
   using L = Layout<KV != PA_BF16>;
@@ -1002,7 +1116,7 @@ inline cudaError_t launch_bs(const TreeArgs& a, const Workspace& ws, cudaStream_
                                         pf::make_kv_map(&vm, a.v_cache, rows, BS)
                                   : pf::make_kv8_map(&km, a.k_cache, rows, BS) &&
                                         pf::make_kv8_map(&vm, a.v_cache, rows, BS);
-  if (!maps || !pf::make_q_map(&qm, a.q, a.num_tokens, a.num_q_heads, a.group))
+  if (!maps || !make_q_map(&qm, a))
     return cudaErrorInvalidValue;
   static tc::DeviceCache slots;
   int per_sm = 0;

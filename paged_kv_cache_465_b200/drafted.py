@@ -7,25 +7,29 @@ stays on the GPU: no call synchronises, so a step can be captured in a CUDA grap
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Sequence
 
 from . import (PARTITION_AUTO, PA_ERR_WORKSPACE, PA_OK, PagedAttnError, _dtype_code, _lib, _torch,
                pa_decode_desc, pa_rotary_desc)
 
 
-def _ptr(x, name, dtype, dev, shape=None):
-    """Device pointer of a contiguous tensor of this type (and shape) on device ``dev``."""
-    if not x.is_cuda:
+def _refuse(x, name, dtype, dev, shape):
+    if x.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if x.get_device() != dev:
         raise ValueError(f"{name} is on another device")
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError(f"{name} has dtype {x.dtype}, expected {dtype}")
     if shape is not None and x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(x, name, dtype, dev, shape=None):
+    """Device pointer of a contiguous tensor of this type (and shape) on device ``dev``."""
+    if x.get_device() != dev or x.dtype is not dtype or not x.is_contiguous() or \
+            (shape is not None and x.shape != shape):
+        _refuse(x, name, dtype, dev, shape)
     return x.data_ptr()
 
 
@@ -38,22 +42,25 @@ def _launch(fn, what: str, dev: int, stream, args) -> None:
     stream as its last argument."""
     torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        handle = torch.cuda.current_stream(dev).cuda_stream
     elif stream.device.index != dev:
         raise ValueError("stream belongs to another device than the tensors")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        st = fn(*args, stream.cuda_stream)
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, handle)
     if st != PA_OK:
         raise PagedAttnError(st, what)
 
 
 def _device(x, name) -> int:
-    if not x.is_cuda:
+    dev = x.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return x.get_device()
+    return dev
 
 
 def _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev):
@@ -66,24 +73,6 @@ def _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev):
             _opt(k_zeros, "k_zeros", i32, dev, bh), _opt(v_zeros, "v_zeros", i32, dev, bh))
     return _dtype_code(k_cache.dtype), (_ptr(k_cache, "k_cache", k_cache.dtype, dev),
                                         _ptr(v_cache, "v_cache", k_cache.dtype, dev)), side
-
-
-def _apart(inputs, outputs) -> None:
-    """Outputs share no memory with one another or with an input (None: absent)."""
-    spans = []
-    for kind, xs in (("in", inputs), ("out", outputs)):
-        for x in xs:
-            if x is not None and x.numel():
-                a = x.data_ptr()
-                spans.append((a, a + x.numel() * x.element_size(), kind))
-    spans.sort()
-    end = out_end = 0  # how far any buffer so far reaches, and any output
-    for a, b, kind in spans:
-        if a < out_end or (kind == "out" and a < end):
-            raise ValueError("an output overlaps another buffer of the call")
-        end = max(end, b)
-        if kind == "out":
-            out_end = max(out_end, b)
 
 
 def build_step(context_lens, new_lens, blocks_held, block_tables, free_blocks, queue_state, *,
@@ -125,9 +114,6 @@ def build_step(context_lens, new_lens, blocks_held, block_tables, free_blocks, q
         _opt(positions, "positions", i32, dev, (rows,)),
         _opt(tree_mask, "tree_mask", i32, dev, (rows, words)),
         _opt(status, "status", i32, dev, (1,)))
-    _apart((context_lens, new_lens, blocks_held, parents, free_blocks, queue_state),
-           (block_tables, total_lens, query_start, blocks_held_out, queue_state_out, slot_mapping,
-            positions, tree_mask, status))
     _launch(_lib.paged_build_step, "paged_build_step", dev, stream, args)
 
 
@@ -150,22 +136,18 @@ def release_blocks(keep_lens, blocks_held, block_tables, free_blocks, queue_stat
         free_blocks.numel(), _ptr(blocks_held_out, "blocks_held_out", i32, dev, (S,)),
         _ptr(queue_state_out, "queue_state_out", i32, dev, (2,)),
         _opt(status, "status", i32, dev, (1,)))
-    _apart((keep_lens, blocks_held, block_tables, queue_state),
-           (free_blocks, blocks_held_out, queue_state_out, status))
     _launch(_lib.paged_release_blocks, "paged_release_blocks", dev, stream, args)
 
 
-def _rows_ptr(x, name, dtype, dev, heads: int, d: int) -> int:
-    """Pointer of rows [T, heads, d] that may be strided along T."""
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if x.get_device() != dev:
-        raise ValueError(f"{name} is on another device")
-    if x.dtype != dtype:
-        raise TypeError(f"{name} has dtype {x.dtype}, expected {dtype}")
-    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+def _rows(x, name, dtype, dev):
+    """(pointer, token stride) of rows [T, heads, d] that may be strided along T."""
+    T, heads, d = x.shape
+    st = x.stride()
+    if x.get_device() != dev or x.dtype is not dtype:
+        _refuse(x, name, dtype, dev, None)
+    if st[2] != 1 or (heads > 1 and st[1] != d):
         raise ValueError(f"{name} rows must be contiguous [heads, d]")
-    return x.data_ptr()
+    return x.data_ptr(), st[0] if T > 1 else heads * d  # a single row has no stride of its own
 
 
 def rotary_and_cache(q, k, v, q_out, k_cache, v_cache, positions, slot_mapping, inv_freq, *,
@@ -193,20 +175,15 @@ def rotary_and_cache(q, k, v, q_out, k_cache, v_cache, positions, slot_mapping, 
         raise ValueError("positions must be [T], or [axes, T] with a section for each of 1 to 4 axes")
     code, pools, side = _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev)
     dt = q.dtype
-    qp, op = _rows_ptr(q, "q", dt, dev, Hq, d), _rows_ptr(q_out, "q_out", dt, dev, Hq, d)
-    # a single row has no stride of its own
-    qs, ks, vs, os_ = (x.stride(0) if T > 1 else x.shape[1] * d for x in (q, k, v, q_out))
-    if op != qp and T:
-        size, row = q.element_size(), Hq * d
-        if qp < op + ((T - 1) * os_ + row) * size and op < qp + ((T - 1) * qs + row) * size:
-            raise ValueError("q_out overlaps q without being q")
-    desc = pa_rotary_desc(T, Hq, Hkv, d, 2 * half, axes, (ctypes.c_int * 4)(*sec),
-                          adjacent_pairs, B, NB, qs, ks, vs, os_, _dtype_code(dt), code)
+    (qp, qs), (kp, ks) = _rows(q, "q", dt, dev), _rows(k, "k", dt, dev)
+    (vp, vs), (op, os_) = _rows(v, "v", dt, dev), _rows(q_out, "q_out", dt, dev)
+    desc = pa_rotary_desc(T, Hq, Hkv, d, 2 * half, axes, sec, adjacent_pairs, B, NB, qs, ks, vs,
+                          os_, _dtype_code(dt), code)
     _launch(_lib.rotary_and_cache, "rotary_and_cache", dev, stream, (
-        qp, _rows_ptr(k, "k", dt, dev, Hkv, d), _rows_ptr(v, "v", dt, dev, Hkv, d), op, *pools,
+        qp, kp, vp, op, *pools,
         _ptr(positions, "positions", torch.int32, dev, (T,) if positions.dim() == 1 else (axes, T)),
         _ptr(slot_mapping, "slot_mapping", torch.int64, dev, (T,)),
-        _ptr(inv_freq, "inv_freq", torch.float32, dev, (half,)), ctypes.byref(desc), *side))
+        _ptr(inv_freq, "inv_freq", torch.float32, dev, (half,)), desc, *side))
 
 
 def _tree_desc(q, k_cache, block_tables) -> pa_decode_desc:
@@ -223,7 +200,7 @@ def tree_workspace_size(q, k_cache, block_tables, *, max_query_len: int,
                         max_context_len: int) -> int:
     """Workspace bytes of a ``paged_attn_tree`` call with tensors of these shapes and types."""
     return int(_lib.paged_attn_tree_workspace_size(
-        ctypes.byref(_tree_desc(q, k_cache, block_tables)), q.shape[0], max_query_len,
+        _tree_desc(q, k_cache, block_tables), q.shape[0], max_query_len,
         max_context_len))
 
 
@@ -251,7 +228,7 @@ def paged_attn_tree(q, k_cache, v_cache, block_tables, context_lens, query_start
         _ptr(context_lens, "context_lens", i32, dev, (S,)),
         _ptr(query_start, "query_start", i32, dev, (S + 1,)),
         _ptr(tree_mask, "tree_mask", i32, dev, (T, words)), words, T, max_query_len, scale,
-        _ptr(out, "out", q.dtype, dev, q.shape), ctypes.byref(desc), max_context_len, *side,
+        _ptr(out, "out", q.dtype, dev, q.shape), desc, max_context_len, *side,
         _opt(lse_out, "lse_out", torch.float32, dev, (T, Hq)),
         None if workspace is None else _ptr(workspace, "workspace", workspace.dtype, dev),
         0 if workspace is None else workspace.numel() * workspace.element_size())
@@ -259,7 +236,7 @@ def paged_attn_tree(q, k_cache, v_cache, block_tables, context_lens, query_start
         _launch(_lib.paged_attn_tree, "paged_attn_tree", dev, stream, args)
     except PagedAttnError as e:
         if e.status == PA_ERR_WORKSPACE:
-            need = _lib.paged_attn_tree_workspace_size(ctypes.byref(desc), T, max_query_len,
+            need = _lib.paged_attn_tree_workspace_size(desc, T, max_query_len,
                                                        max_context_len)
             raise PagedAttnError(e.status, f"paged_attn_tree needs {need} workspace bytes") from None
         raise
@@ -291,8 +268,6 @@ def tree_verify(parents, draft_tokens, target_tokens, query_start, context_lens,
         _ptr(num_accepted, "num_accepted", i32, dev, (S,)),
         _ptr(next_tokens, "next_tokens", i64, dev, (S,)),
         _ptr(kept_lens, "kept_lens", i32, dev, (S,)))
-    _apart((parents, draft_tokens, target_tokens, query_start, context_lens),
-           (accepted, num_accepted, next_tokens, kept_lens))
     _launch(_lib.tree_verify, "tree_verify", dev, stream, args)
 
 

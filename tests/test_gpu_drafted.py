@@ -220,7 +220,7 @@ def test_bookkeeping_refuses_shared_buffers(pa):
         pa.build_step(z(2), z(2), held, z(6).view(2, 3), z(9), queue, block_size=16, num_blocks=9, **a)
     for kw in (dict(blocks_held_out=held), dict(queue_state_out=queue), dict(total_lens=held),
                dict(positions=slots.view(torch.int32)[4:])):
-        with pytest.raises(ValueError):
+        with pytest.raises(pa.PagedAttnError):
             go(**kw)
     for kw in (dict(query_start=z(2)), dict(positions=z(3)), dict(status=z(2)),
                dict(tree_mask=z(4).view(4, 1).t()), dict(total_lens=z(4)[::2])):
@@ -228,7 +228,7 @@ def test_bookkeeping_refuses_shared_buffers(pa):
             go(**kw)
     with pytest.raises(TypeError):
         go(slot_mapping=z(4))
-    with pytest.raises(ValueError):
+    with pytest.raises(pa.PagedAttnError):
         pa.release_blocks(z(2), held, z(6).view(2, 3), z(9), queue, block_size=16,
                           blocks_held_out=held, queue_state_out=z(2))
 
@@ -365,7 +365,7 @@ def test_rotary_bad_slots_and_zero_points(pa):
         pa.rotary_and_cache(q, k, k, q.flatten()[8:].new_zeros(1).expand(T, hq, d), kc, vc, cuda([1, 2, 3]),
                             slots, inv, k_scales=sc, v_scales=sc, k_zeros=zp, v_zeros=zp)
     buf = torch.zeros(T * hq * d + 64, device="cuda").bfloat16()
-    with pytest.raises(ValueError):   # q_out overlaps q without being q
+    with pytest.raises(pa.PagedAttnError):   # q_out overlaps q without being q
         pa.rotary_and_cache(buf[:T * hq * d].view(T, hq, d), k, k, buf[64:].view(T, hq, d), kc, vc,
                             cuda([1, 2, 3]), slots, inv, k_scales=sc, v_scales=sc, k_zeros=zp, v_zeros=zp)
 

@@ -157,26 +157,36 @@ def test_compact_moves_in_order_and_requantises():
 
 def test_refusals_without_a_device(pa):
     lib, one, nul = pa._lib, ctypes.c_void_p(256), ctypes.c_void_p(0)
-    two, three, four = (ctypes.c_void_p(256 + 4096 * i) for i in (1, 2, 3))
+    two = ctypes.c_void_p(256 + 4096)
+    apart = [ctypes.c_void_p(4096 * (i + 1)) for i in range(20)]   # addresses of separate buffers
 
-    def build(seqs=2, width=4, bs=16, nb=8, cap=8, rows=8, words=2, ptr=one, held_out=two,
-              queue_out=three, total=four):
-        return lib.paged_build_step(ptr, ptr, ptr, nul, ptr, ptr, ptr, seqs, width, bs, nb, cap,
-                                    rows, words, total, one, held_out, queue_out, one, nul, one,
-                                    nul, nul)
+    def build(seqs=2, width=4, bs=16, nb=8, cap=8, rows=8, words=2, **at):
+        p = list(apart[:15])   # 0-6 inputs (3 parents, 4 tables), 7-14 outputs
+        for k, v in at.items():
+            p[int(k[1:])] = v
+        return lib.paged_build_step(*p[:7], seqs, width, bs, nb, cap, rows, words, *p[7:15], nul)
     for kw in (dict(seqs=-1), dict(seqs=65536), dict(width=0), dict(bs=0), dict(nb=0), dict(cap=0),
-               dict(rows=-1), dict(words=0), dict(words=9), dict(ptr=nul), dict(held_out=one),
-               dict(queue_out=one), dict(total=one), dict(width=1 << 30)):
+               dict(rows=-1), dict(words=0), dict(words=9), dict(width=1 << 30)):
         assert build(**kw) == pa.PA_ERR_INVALID, kw
-    assert build(seqs=0, ptr=nul) == pa.PA_OK
+    for i in (0, 1, 2, 4, 5, 6, 7, 8, 9, 10, 11):                # required
+        assert build(**{f"p{i}": nul}) == pa.PA_ERR_INVALID, i
+    for i, j in ((4, 0), (7, 0), (7, 1), (9, 2), (10, 6), (11, 3), (12, 11), (13, 5), (14, 8)):
+        assert build(**{f"p{i}": apart[j]}) == pa.PA_ERR_INVALID, (i, j)      # shared memory
+    assert build(p12=ctypes.c_void_p(4096 * 12 + 63)) == pa.PA_ERR_INVALID   # partly
+    assert build(seqs=0, p0=nul) == pa.PA_OK
 
-    def release(seqs=2, width=4, bs=16, cap=8, ptr=one, held_out=two, queue_out=three):
-        return lib.paged_release_blocks(ptr, ptr, ptr, ptr, ptr, seqs, width, bs, cap, held_out,
-                                        queue_out, nul, nul)
-    for kw in (dict(seqs=-1), dict(width=0), dict(bs=0), dict(cap=0), dict(ptr=nul),
-               dict(held_out=one), dict(queue_out=one)):
+    def release(seqs=2, width=4, bs=16, cap=8, **at):
+        p = list(apart[:8])   # 0-4 inputs (3 the ring), 5-7 outputs
+        for k, v in at.items():
+            p[int(k[1:])] = v
+        return lib.paged_release_blocks(*p[:5], seqs, width, bs, cap, *p[5:8], nul)
+    for kw in (dict(seqs=-1), dict(width=0), dict(bs=0), dict(cap=0)):
         assert release(**kw) == pa.PA_ERR_INVALID, kw
-    assert release(seqs=0, ptr=nul) == pa.PA_OK
+    for i in range(7):
+        assert release(**{f"p{i}": nul}) == pa.PA_ERR_INVALID, i
+    for i, j in ((5, 1), (5, 0), (6, 4), (7, 5), (3, 2)):
+        assert release(**{f"p{i}": apart[j]}) == pa.PA_ERR_INVALID, (i, j)
+    assert release(seqs=0, p0=nul) == pa.PA_OK
 
     def rotary(T=4, hq=8, hkv=2, d=128, rot=128, axes=1, sec=(64, 0, 0, 0), nb=8, bs=16, qs=1024,
                ks=256, indt=pa.PA_BF16, cache=pa.PA_BF16, ptr=one, q_out=two, sc=nul, zp=nul,
@@ -219,11 +229,18 @@ def test_refusals_without_a_device(pa):
         assert tree(ptr=nul, ws=nul, **kw) == pa.PA_OK
     assert lib.paged_attn_tree_workspace_size(ctypes.byref(split), 100, 50, 1024) == 0
 
-    def verify(S=2, T=8, A=4, ptr=one):
-        return lib.tree_verify(ptr, ptr, ptr, ptr, ptr, S, T, A, ptr, ptr, ptr, ptr, nul)
-    for kw in (dict(S=-1), dict(S=65536), dict(T=-1), dict(A=0), dict(ptr=nul)):
+    def verify(S=2, T=8, A=4, **at):
+        p = list(apart[:9])   # 0-4 inputs, 5-8 outputs
+        for k, v in at.items():
+            p[int(k[1:])] = v
+        return lib.tree_verify(*p[:5], S, T, A, *p[5:9], nul)
+    for kw in (dict(S=-1), dict(S=65536), dict(T=-1), dict(A=0)):
         assert verify(**kw) == pa.PA_ERR_INVALID, kw
-    assert verify(S=0, ptr=nul) == pa.PA_OK
+    for i in range(9):
+        assert verify(**{f"p{i}": nul}) == pa.PA_ERR_INVALID, i
+    for i, j in ((5, 0), (6, 3), (7, 1), (8, 4), (8, 6)):
+        assert verify(**{f"p{i}": apart[j]}) == pa.PA_ERR_INVALID, (i, j)
+    assert verify(S=0, p0=nul) == pa.PA_OK
 
     def compact(S=2, A=4, width=4, hkv=2, hd=128, bs=16, nb=8, dt=pa.PA_BF16, ptr=one, sc=nul, zp=nul):
         return lib.compact_accepted(ptr, ptr, ptr, ptr, ptr, ptr, ptr, S, A, width, hkv, hd, bs, nb,
