@@ -24,10 +24,17 @@
 //   warp 4       tcgen05.mma, one lane: S(g + 1) = Q K^T into one of two buffers in tensor
 //                memory while S(g) is in softmax, then O += P(g) V, P read from tensor memory;
 //   warps 0-3    softmax, one thread per row (= tensor-memory lane): mask, running maximum
-//                with lazy rescaling, P as bf16 pairs over S; O / l or the partial at the end;
-//   warps 6-9    fp8 / int8 caches: turn the codes that TMA staged into the bf16 tiles the
-//                products read (exact values; scales go to the scores and to P).
+//                with lazy rescaling, P as 16-bit pairs over S; O / l or the partial at the end;
+//   warps 6-9    fp8 / int8 caches: turn the codes that TMA staged into the f16 tiles the
+//                products read (exact values; scales go to the scores and to P), and Q into f16.
 // Two CTAs per SM hide each other's starts, ends and waits.
+//
+// Types: a bf16 cache is multiplied as it is, with P rounded to bf16. Codes of one byte become
+// f16 (one instruction per two E4M3 codes; bf16 takes five and made the converters the limit):
+// E4M3 values and code - zero are exact in f16. Q rows are brought to [2^14, 2^15) by a power
+// of two each, which bf16's eight bits survive down to 2^-28 of the row's largest element. P
+// carries V scale / v_ref * 2^7, v_ref a power of two no smaller than any V scale so far: at
+// most 2^15, and f16 holds it to 11 bits down to 2^-21 of the largest (bf16 would hold 8).
 //
 // Every wait is bounded; a CTA that gives up flags PA_DEVERR_TIMEOUT, lets its copies and
 // products finish and releases its tensor memory.
@@ -90,6 +97,7 @@ struct TileInfo {
   int flags;        // first / last tile of its piece; the run is over; the piece is a whole pair
   uint32_t bad;     // bit b: block b of the tile cannot be read
   int key0;         // position of the tile's first key
+  // of the piece, and only in its first tile's slot:
   int base, ctx;    // context without and with the step's rows
   int row0, rows;   // first token row of the row tile, its tokens
   int s, kvh;
@@ -97,6 +105,23 @@ struct TileInfo {
   float ks[kMaxTileBlocks], vs[kMaxTileBlocks];
   int kz[kMaxTileBlocks], vz[kMaxTileBlocks];
 };
+
+// A piece of a run: key tiles [t0, t1) of row tile rt, sequence s, kv head kvh.
+struct Piece {
+  int rt, s, kvh, t0, t1, tiles;
+  int q0, n, ctx;
+};
+
+// Up to 32 consecutive blocks of a piece on their way to the producer (a ring of windows in
+// shared memory that asynchronous copies fill): block ids, then their scales.
+struct Window {
+  int id[32];       // -1: cannot be read, or none
+  float ks[32], vs[32];
+  int kz[32], vz[32];
+  Piece pc;
+  int tile0, ntiles, first, any;   // its key tiles; first of its piece; exists
+};
+constexpr int kWindows = 4;
 
 template <bool QUANT>
 struct Layout {
@@ -111,8 +136,10 @@ struct Layout {
   static constexpr int kOffK8 = kOffV + kVSt * kKVBytes;
   static constexpr int kOffV8 = kOffK8 + kK8St * kCodeBytes;
   static constexpr int kOffInfo = kOffV8 + kV8St * kCodeBytes;
-  static constexpr int kOffMisc = kOffInfo + kInfo * (int)sizeof(TileInfo);
-  static constexpr int kOffBar = kOffMisc + 384;
+  static constexpr int kOffWin = kOffInfo + kInfo * (int)sizeof(TileInfo);
+  static constexpr int kOffMisc = kOffWin + kWindows * (int)sizeof(Window);
+  static constexpr int kOffDown = kOffMisc + 384;          // float [4][kRows]: what undoes Q's factors
+  static constexpr int kOffBar = kOffDown + (QUANT ? 4 * kRows * 4 : 0);
   // barriers
   static constexpr int kBarQF = 0, kBarQE = 2;   // [2] each
   static constexpr int kBarKF = 4, kBarKE = kBarKF + kKSt;
@@ -123,20 +150,23 @@ struct Layout {
   static constexpr int kBarInfo = kBarO + 2;     // [kInfo]
   static constexpr int kBarK8F = kBarInfo + kInfo, kBarK8E = kBarK8F + kK8St;
   static constexpr int kBarV8F = kBarK8E + kK8St, kBarV8E = kBarV8F + kV8St;
-  static constexpr int kBarSm = kBarV8E + kV8St;  // the four softmax warps, once a piece
+  static constexpr int kBarQR = kBarV8E + kV8St;  // [4] Q converted
+  static constexpr int kBarSm = kBarQR + (QUANT ? 4 : 0);  // the four softmax warps, once a piece
   static constexpr int kBarFin = kBarSm + 1;
   static constexpr int kNumBars = kBarFin + 1;
   static constexpr int kSmem = kOffBar + 8 * kNumBars + 1024;  // + alignment slack
 };
 static_assert(Layout<true>::kSmem <= 113 * 1024 && Layout<false>::kSmem <= 113 * 1024,
               "two CTAs per SM");
-static_assert(kInfo * sizeof(TileInfo) % 8 == 0, "barriers are 8-byte aligned");
+static_assert((kInfo * sizeof(TileInfo) + kWindows * sizeof(Window)) % 8 == 0,
+              "barriers are 8-byte aligned");
 
 // S = Q K^T: A and B K-major, N = 64 keys. O += P V: A from tensor memory, B MN-major, N = 128.
-constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kKeys >> 3) << 17) |
-                             ((uint32_t)(kRows >> 4) << 24);
-constexpr uint32_t kIdescPV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
-                              ((uint32_t)(kDim >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+// Both operands bf16 (1 << 7, 1 << 10), or both f16.
+constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
+constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(kDim >> 3) << 17) |
+                              ((uint32_t)(kRows >> 4) << 24);
 
 // Workspace: what CTA b's run is, then the partial pieces.
 struct RunInfo {
@@ -164,11 +194,12 @@ inline Workspace workspace_at(void* p) {
   return w;
 }
 
-// A piece of a run: key tiles [t0, t1) of row tile rt, sequence s, kv head kvh.
-struct Piece {
-  int rt, s, kvh, t0, t1, tiles;
-  int q0, n, ctx;
-};
+// A four-byte asynchronous copy into shared memory, or four zero bytes.
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool go) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(go ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ int tiles_of(int ctx) { return (ctx + kKeys - 1) / kKeys; }
 __device__ __forceinline__ int row_tiles_of(int n, int G) {
@@ -299,36 +330,13 @@ __device__ __forceinline__ uint64_t tile_view(const TreeArgs& a, int64_t row, in
   return v;
 }
 
-// Four E4M3 codes -> bf16 (exact). Sign, exponent and fraction move to their bf16 places, which
-// makes the value 2^-120 times too small; bf16 keeps subnormals, so one product restores
-// E4M3's as well. The two NaN codes come out as +-480: the caller looks for them.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-  lo = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
-  hi = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
-  const uint32_t up = 0x7b807b80u;  // 2^120, twice
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(up));
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(up));
-}
-// Four int8 codes -> bf16 of code - zero (exact: at most 255 in size). The code + 128 becomes
-// the low byte of the float 2^23 + code + 128; z = 2^23 + 128 + zero.
-__device__ __forceinline__ void i8x4_to_bf16(uint32_t w, float z, uint32_t& lo, uint32_t& hi) {
-  w ^= 0x80808080u;
-  float f[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    f[e] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + e)) - z;
-  lo = pack_bf16x2(f[0], f[1]);
-  hi = pack_bf16x2(f[2], f[3]);
-}
-
 // The softmax of one tile for one row: S (64 columns of this lane in tensor memory at `sbuf`) to
-// P (bf16 pairs over its first 32 columns). Two passes of 32 columns each over S, which keeps
+// P (16-bit pairs over its first 32 columns; rvs: the factor of the V scales). Two passes of 32 columns each over S, which keeps
 // half the registers and code of one pass that holds all 64. `view`: keys the row sees (read
 // only when MASKED). Returns the factor that O and l have to be multiplied with.
 template <int BS, bool QUANT, bool MASKED>
 __device__ __forceinline__ float softmax_tile(uint32_t sbuf, const TileInfo& ti, float sl2,
-                                              uint64_t view, float& m_used, float& l) {
+                                              float rvs, uint64_t view, float& m_used, float& l) {
   float m_new = m_used;
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
@@ -371,11 +379,11 @@ __device__ __forceinline__ float softmax_tile(uint32_t sbuf, const TileInfo& ti,
       sum[e & 3] += p0;
       sum[(e + 1) & 3] += p1;
       if constexpr (QUANT) {  // P carries its block's V scale; a key that is not seen, none
-        const float vs = ti.vs[c * (32 / BS) + e / BS];
+        const float vs = ti.vs[c * (32 / BS) + e / BS] * rvs;
         p0 = MASKED && p0 == 0.f ? 0.f : p0 * vs;
         p1 = MASKED && p1 == 0.f ? 0.f : p1 * vs;
       }
-      pk[e >> 1] = pack_bf16x2(p0, p1);
+      pk[e >> 1] = QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
     }
     pf::tmem_st16(sbuf + c * 16, pk);  // over columns that both passes have read
   }
@@ -422,7 +430,8 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       if (QUANT && ((i >= L::kBarKF && i < L::kBarKF + L::kKSt) ||
                     (i >= L::kBarVF && i < L::kBarVF + L::kVSt) ||
                     (i >= L::kBarK8E && i < L::kBarK8E + L::kK8St) ||
-                    (i >= L::kBarV8E && i < L::kBarV8E + L::kV8St)))
+                    (i >= L::kBarV8E && i < L::kBarV8E + L::kV8St) ||
+                    (i >= L::kBarQR && i < L::kBarQR + 4)))
         count = 32 * kConvWarps;
       mbar_init(bar(i), count);
     }
@@ -502,67 +511,75 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
 
   if (warp == kTmaWarp) {
     // ------------------------------ producer ------------------------------
-    // A window is up to 32 consecutive blocks of a piece, lane b holding block b.
-    struct Window {
-      int p;             // block id; -1: unreadable or none
-      float ks, vs;
-      int kz, vz;
-      int tile0, ntiles; // its key tiles within the piece
-      Piece pc;
-      bool first, any;   // first of its piece; exists
-    };
+    // Windows pass through three stages, so that nothing is waited for as soon as it is asked
+    // for: window w is in use, the scales of w + 1 and the block ids of w + 2 are on their way.
+    Window* win = reinterpret_cast<Window*>(smem + L::kOffWin);
     Walk walk;
     walk.start(a, s_start[0] >= 0 ? count : 0, s_start[0], s_start[1], s_start[2], s_start[3]);
-    Window cur, nxt;
-    nxt.pc.t1 = 0;
-    int wt = 0;          // next tile of the piece in nxt
-    bool run_first = true;
-    nxt.any = true;
+    Piece pc;
+    pc.t1 = 0;
+    int wt = 0;          // next tile of the piece that the newest window belongs to
+    bool more = true, run_first = true;
     const uint64_t keep = tc::evict_first_policy();
     int g = 0, pieces = 0;
-    // fetches the window behind the one in nxt (block ids and scales, used a window later)
-    auto next_window = [&]() {
-      if (!nxt.any) return;
-      nxt.first = wt == nxt.pc.t1;
-      if (nxt.first) {
-        nxt.any = walk.next(a, nxt.pc);
-        if (!nxt.any) return;
-        wt = nxt.pc.t0;
+    auto fetch_ids = [&](int i) {
+      Window& w = win[i % kWindows];
+      const bool first = wt == pc.t1;
+      if (more && first) {
+        more = walk.next(a, pc);
+        wt = pc.t0;
       }
-      nxt.tile0 = wt;
-      nxt.ntiles = min(WT, nxt.pc.t1 - wt);
-      wt += nxt.ntiles;
-      nxt.p = -1;
-      nxt.ks = nxt.vs = 1.f;
-      nxt.kz = nxt.vz = 0;
-      const int blk = nxt.tile0 * NB + lane;
-      if (lane < nxt.ntiles * NB && blk * BS < nxt.pc.ctx) {
-        int p = a.block_tables[(int64_t)nxt.pc.s * a.max_blocks_per_seq + blk];
-        if (p < 0 || p >= a.num_blocks) {
-          flag_error(PA_DEVERR_BLOCK_ID);
-          p = -1;
-        } else if constexpr (QUANT) {
-          const int64_t bh = (int64_t)p * Hkv + nxt.pc.kvh;
-          nxt.ks = a.k_scales[bh];
-          nxt.vs = a.v_scales[bh];
-          if constexpr (KV == PA_INT8) {
-            nxt.kz = a.k_zeros[bh];
-            nxt.vz = a.v_zeros[bh];
-            if (!zero_in_range(nxt.kz) || !zero_in_range(nxt.vz)) {
-              flag_error(PA_DEVERR_ZERO);
-              p = -1;
-            }
-          }
+      const int n = min(WT, pc.t1 - wt), blk = wt * NB + lane;
+      if (lane == 0) {
+        w.pc = pc;
+        w.tile0 = wt;
+        w.ntiles = n;
+        w.first = first;
+        w.any = more;
+      }
+      const bool want = more && lane < n * NB && blk * BS < pc.ctx;
+      copy4(&w.id[lane], a.block_tables + (want ? (int64_t)pc.s * a.max_blocks_per_seq + blk : 0), want);
+      wt += n;
+    };
+    auto fetch_scales = [&](int i) {
+      Window& w = win[i % kWindows];
+      int p = w.id[lane];
+      const bool want = w.any && lane < w.ntiles * NB && (w.tile0 * NB + lane) * BS < w.pc.ctx;
+      if (want && (p < 0 || p >= a.num_blocks)) flag_error(PA_DEVERR_BLOCK_ID);
+      if (!want || p < 0 || p >= a.num_blocks) p = -1;
+      w.id[lane] = p;
+      if constexpr (QUANT) {  // zero scales for what is not there: P's reference ignores it
+        const int64_t bh = p >= 0 ? (int64_t)p * Hkv + w.pc.kvh : 0;
+        copy4(&w.ks[lane], a.k_scales + bh, p >= 0);
+        copy4(&w.vs[lane], a.v_scales + bh, p >= 0);
+        if constexpr (KV == PA_INT8) {
+          copy4(&w.kz[lane], a.k_zeros + bh, p >= 0);
+          copy4(&w.vz[lane], a.v_zeros + bh, p >= 0);
         }
-        nxt.p = p;
       }
     };
-    next_window();
-    cur = nxt;
-    next_window();
+    fetch_ids(0);
+    copies_done();
+    __syncwarp();
+    fetch_scales(0);
+    fetch_ids(1);
 #pragma unroll 1
-    while (ok && cur.any) {
-      if (cur.first) {
+    for (int i = 0;; ++i) {
+      copies_done();
+      __syncwarp();
+      Window& w = win[i % kWindows];
+      if (!w.any) break;
+      if (KV == PA_INT8 && w.id[lane] >= 0 &&
+          (!zero_in_range(w.kz[lane]) || !zero_in_range(w.vz[lane]))) {
+        flag_error(PA_DEVERR_ZERO);
+        w.id[lane] = -1;
+        w.vs[lane] = 0.f;
+      }
+      fetch_scales(i + 1);
+      fetch_ids(i + 2);
+      __syncwarp();
+      const int kvh = w.pc.kvh, ctx = w.pc.ctx, tile0 = w.tile0, ntiles = w.ntiles;
+      if (w.first) {
         // the last S product of the piece that used this buffer has read it
         const int qb = q_bufs == 2 ? pieces & 1 : 0, use = q_bufs == 2 ? pieces >> 1 : pieces;
         if (use > 0) ok = wait_all(bar(L::kBarQE + qb), (use - 1) & 1);
@@ -572,92 +589,108 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
           mbar_arrive_tx(bar(L::kBarQF + qb), 2 * slab);
 #pragma unroll 1
           for (int h = 0; h < 2; ++h)
-            pf::tma_load_4d(sQ + (2 * qb + h) * slab, &qmap, 0, h, cur.pc.kvh * G,
-                            cur.pc.q0 + cur.pc.rt * TM, bar(L::kBarQF + qb), keep);
+            pf::tma_load_4d(sQ + (2 * qb + h) * slab, &qmap, 0, h, kvh * G,
+                            w.pc.q0 + w.pc.rt * TM, bar(L::kBarQF + qb), keep);
         }
         __syncwarp();
         ++pieces;
       }
+      // Lane l copies block l of the window whenever its tile's turn comes. What the whole
+      // window shares is worked out here: a tile's own code is kept to a few instructions.
+      const int p = w.id[lane], mine = lane / NB, row = (p * Hkv + kvh) * BS;
+      const uint32_t good = __ballot_sync(0xffffffffu, p >= 0);
+      const uint32_t gone = __ballot_sync(0xffffffffu, p < 0 && lane < ntiles * NB &&
+                                                           (tile0 * NB + lane) * BS < ctx);
+      const uint32_t off = (uint32_t)(lane & (NB - 1)) * BS * 128;
+      float ks = 0.f, vs = 0.f;
+      int kz = 0, vz = 0;
+      if constexpr (QUANT) {
+        ks = w.ks[lane];
+        vs = w.vs[lane];
+        if constexpr (KV == PA_INT8) {
+          kz = w.kz[lane];
+          vz = w.vz[lane];
+        }
+      }
+      const int last_tile = w.pc.t1 - 1 - tile0;
+      const int whole = w.pc.t0 == 0 && w.pc.t1 == w.pc.tiles ? kWhole : 0;
 #pragma unroll 1
-      for (int k = 0; k < cur.ntiles; ++k, ++g) {
-        // this tile's blocks sit in lanes k * NB ..
-        const int src = (k * NB + (lane & (NB - 1))) & 31, tile = cur.tile0 + k;
-        const int p = __shfl_sync(0xffffffffu, cur.p, src);
-        const bool exists = tile * kKeys + (lane & (NB - 1)) * BS < cur.pc.ctx;
-        const uint32_t good = __ballot_sync(0xffffffffu, lane < NB && p >= 0);
-        const uint32_t bad = __ballot_sync(0xffffffffu, lane < NB && p < 0 && exists);
-        const int pb = __shfl_sync(0xffffffffu, p, (lane >> 1) & (NB - 1));
-        // ---- K, then V: the ring's stage is free once its last reader is done ----
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const int nst = QUANT ? (kv ? L::kV8St : L::kK8St) : (kv ? L::kVSt : L::kKSt);
-          const int full = QUANT ? (kv ? L::kBarV8F : L::kBarK8F) : (kv ? L::kBarVF : L::kBarKF);
-          const int empty = QUANT ? (kv ? L::kBarV8E : L::kBarK8E) : (kv ? L::kBarVE : L::kBarKE);
+      for (int k = 0; k < ntiles; ++k, ++g) {
+        const uint32_t bytes = (uint32_t)__popc((good >> (k * NB)) & ((1u << NB) - 1u)) * BS * 128u;
+        const bool my_turn = mine == k && p >= 0;
+        TileInfo& ti = info[g % kInfo];
+        // ---- K: the ring's stage is free once its last reader is done ----
+        {
+          constexpr int nst = QUANT ? L::kK8St : L::kKSt;
+          constexpr int full = QUANT ? L::kBarK8F : L::kBarKF, empty = QUANT ? L::kBarK8E : L::kBarKE;
           const int st = g % nst;
           if (g >= nst) ok = wait_all(bar(empty + st), ((g / nst) - 1) & 1);
           if (!ok) break;
-          if (kv == 0) {
-            // The slot is free: the stage's K (bf16) or codes (two tiles' conversions later)
-            // could only be read after S(g - 4) at the earliest, which was issued behind
-            // P V (g - 6), so softmax and converters are past tile g - 6 > g - kInfo.
-            TileInfo& ti = info[g % kInfo];
-            if (lane == 0) {
-              const Piece& pc = cur.pc;
-              const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
-              ti.flags = (tile == pc.t0 ? kFirst : 0) | (tile == pc.t1 - 1 ? kLast : 0) |
-                         (whole ? kWhole : 0);
-              ti.bad = bad;
-              ti.key0 = tile * kKeys;
-              ti.base = pc.ctx - pc.n;
-              ti.ctx = pc.ctx;
-              ti.row0 = pc.q0 + pc.rt * TM;
-              ti.rows = min(TM, pc.n - pc.rt * TM);
-              ti.s = pc.s;
-              ti.kvh = pc.kvh;
-              ti.slot = blockIdx.x * 2 + (run_first ? 0 : 1);
-            }
-            if constexpr (QUANT) {
-              const float ks = __shfl_sync(0xffffffffu, cur.ks, src);
-              const float vs = __shfl_sync(0xffffffffu, cur.vs, src);
-              if (lane < NB) {
-                ti.ks[lane] = ks;
-                ti.vs[lane] = vs;
-              }
-              if constexpr (KV == PA_INT8) {
-                const int kz = __shfl_sync(0xffffffffu, cur.kz, src);
-                const int vz = __shfl_sync(0xffffffffu, cur.vz, src);
-                if (lane < NB) {
-                  ti.kz[lane] = kz;
-                  ti.vz[lane] = vz;
-                }
-              }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::kBarInfo + g % kInfo));
-          }
-          const uint32_t fb = bar(full + st);
-          if (lane == 0)
-            mbar_arrive_tx(fb, (uint32_t)__popc(good) * BS * 128u * (QUANT ? 1u : 2u));
+          if (lane == 0) mbar_arrive_tx(bar(full + st), QUANT ? bytes : 2 * bytes);
           __syncwarp();
-          if constexpr (QUANT) {
-            if (lane < NB && p >= 0)
-              tc::tma_load_2d(smem_u32(smem + (kv ? L::kOffV8 : L::kOffK8)) + st * kCodeBytes +
-                                  lane * BS * 128,
-                              kv ? &vmap : &kmap, 0, (p * Hkv + cur.pc.kvh) * BS, fb, keep);
-          } else {
-            if (lane < 2 * NB && pb >= 0)
-              pf::tma_load_3d((kv ? sV : sK) + st * kKVBytes + (lane & 1) * kKVSlab +
-                                  (lane >> 1) * BS * 128,
-                              kv ? &vmap : &kmap, 0, lane & 1, (pb * Hkv + cur.pc.kvh) * BS, fb);
+          if (my_turn) {
+            if constexpr (QUANT) {
+              tc::tma_load_2d(smem_u32(smem + L::kOffK8) + st * kCodeBytes + off, &kmap, 0, row,
+                              bar(full + st), keep);
+            } else {
+              pf::tma_load_3d(sK + st * kKVBytes + off, &kmap, 0, 0, row, bar(full + st));
+              pf::tma_load_3d(sK + st * kKVBytes + kKVSlab + off, &kmap, 0, 1, row, bar(full + st));
+            }
           }
         }
-        if (!ok) break;
+        // The description's slot is free: the stage's K (bf16) or codes (two tiles' conversions
+        // later) could only be read after S(g - 4) at the earliest, which was issued behind
+        // P V (g - 6), so softmax and converters are past tile g - 6 > g - kInfo.
+        if (QUANT && mine == k) {
+          ti.ks[lane & (NB - 1)] = ks;
+          ti.vs[lane & (NB - 1)] = vs;
+          if constexpr (KV == PA_INT8) {
+            ti.kz[lane & (NB - 1)] = kz;
+            ti.vz[lane & (NB - 1)] = vz;
+          }
+        }
+        if (lane == 0) {
+          const bool first = k == 0 && w.first;
+          ti.flags = (first ? kFirst : 0) | (k == last_tile ? kLast : 0) | whole;
+          ti.bad = (gone >> (k * NB)) & ((1u << NB) - 1u);
+          ti.key0 = (tile0 + k) * kKeys;
+          if (first) {
+            ti.base = ctx - w.pc.n;
+            ti.ctx = ctx;
+            ti.row0 = w.pc.q0 + w.pc.rt * TM;
+            ti.rows = min(TM, w.pc.n - w.pc.rt * TM);
+            ti.s = w.pc.s;
+            ti.kvh = kvh;
+            ti.slot = blockIdx.x * 2 + (run_first ? 0 : 1);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarInfo + g % kInfo));
+        // ---- V ----
+        {
+          constexpr int nst = QUANT ? L::kV8St : L::kVSt;
+          constexpr int full = QUANT ? L::kBarV8F : L::kBarVF, empty = QUANT ? L::kBarV8E : L::kBarVE;
+          const int st = g % nst;
+          if (g >= nst) ok = wait_all(bar(empty + st), ((g / nst) - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_tx(bar(full + st), QUANT ? bytes : 2 * bytes);
+          __syncwarp();
+          if (my_turn) {
+            if constexpr (QUANT) {
+              tc::tma_load_2d(smem_u32(smem + L::kOffV8) + st * kCodeBytes + off, &vmap, 0, row,
+                              bar(full + st), keep);
+            } else {
+              pf::tma_load_3d(sV + st * kKVBytes + off, &vmap, 0, 0, row, bar(full + st));
+              pf::tma_load_3d(sV + st * kKVBytes + kKVSlab + off, &vmap, 0, 1, row, bar(full + st));
+            }
+          }
+        }
       }
       if (!ok) break;
-      if (cur.tile0 + cur.ntiles == cur.pc.t1) run_first = false;
-      cur = nxt;
-      next_window();
+      if (w.tile0 + w.ntiles == w.pc.t1) run_first = false;
+      __syncwarp();
     }
+    copies_done();
     if (lane == 0) {
       if (ok) {  // the slot is free as above
         info[g % kInfo].flags = kEnd;
@@ -679,8 +712,12 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
   } else if (warp == kMmaWarp) {
     // ------------------------------ MMA issuer ------------------------------
     int g = 0, pieces = 0, q_buf = 0;   // tiles whose S is issued; pieces whose Q is in use
-    uint32_t q_at = sQ;
+    uint32_t q_lo = 0;                  // low half of Q's descriptor
     uint32_t fresh = 0;                 // bit b: P V from S buffer b begins a piece
+    // Descriptors differ in their low half alone, the address in 16-byte units (which never
+    // carries into the fields above): one addition each.
+    const uint64_t kmajor = sdesc(0, 16, 1024), vmajor = sdesc(0, kKVSlab, 1024);
+    const uint32_t q_slab = (uint32_t)q_rows * 8;
     // S of the run's next tile; false when there is none (or a wait gave up)
     auto next_s = [&]() {
       ok = wait_info(g);
@@ -689,9 +726,10 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       if (flags & kEnd) return false;
       if (flags & kFirst) {
         q_buf = q_bufs == 2 ? pieces & 1 : 0;
-        ok = wait_all(bar(L::kBarQF + q_buf), (q_bufs == 2 ? pieces >> 1 : pieces) & 1);
+        ok = QUANT ? wait_all(bar(L::kBarQR + (pieces & 3)), (pieces >> 2) & 1)
+                   : wait_all(bar(L::kBarQF + q_buf), (q_bufs == 2 ? pieces >> 1 : pieces) & 1);
         if (!ok) return false;
-        q_at = sQ + q_buf * q_rows * 256;
+        q_lo = (sQ >> 4) + q_buf * q_rows * 16;
         ++pieces;
       }
       ok = wait_all(bar(L::kBarKF + g % L::kKSt), (g / L::kKSt) & 1);
@@ -700,12 +738,13 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       const uint32_t b = 1u << (g & 1);
       fresh = (flags & kFirst) ? fresh | b : fresh & ~b;
       if (lane == 0) {
-        const uint32_t kst = sK + (g % L::kKSt) * kKVBytes;
+        const uint64_t kd = kmajor + ((sK + (g % L::kKSt) * kKVBytes) >> 4);
+        const uint64_t qd0 = kmajor + q_lo, qd1 = qd0 + q_slab;
 #pragma unroll
         for (int kk = 0; kk < kDim / 16; ++kk)
-          pf::umma_bf16(tmem + (g & 1) * kKeys,
-                        sdesc(q_at + (kk >> 2) * q_rows * 128 + (kk & 3) * 32, 16, 1024),
-                        sdesc(kst + (kk >> 2) * kKVSlab + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0);
+          pf::umma_bf16(tmem + (g & 1) * kKeys, (kk < 4 ? qd0 : qd1) + (kk & 3) * 2,
+                        kd + (kk >> 2) * (kKVSlab / 16) + (kk & 3) * 2,
+                        kIdescS | (QUANT ? 0 : kBf16), kk > 0);
         umma_commit(bar(L::kBarSF + (g & 1)));
         umma_commit(bar(L::kBarKE + g % L::kKSt));
         if (flags & kLast) umma_commit(bar(L::kBarQE + q_buf));
@@ -714,30 +753,30 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       ++g;
       return true;
     };
+    bool more = next_s();
 #pragma unroll 1
-    for (int j = -1; ok; ++j) {
-      const bool more = next_s();
+    for (int j = 0; ok && j < g; ++j) {
+      // S of tile j + 1 first: it runs while tile j is in softmax. (P V first whenever its
+      // operands were there lost a fifth, the softmax then waits for S; polling for whichever
+      // came first lost 5 %.)
+      if (more) more = next_s();
       if (!ok) break;
-      if (j < 0) {
-        if (!more) break;
-        continue;
-      }
       ok = wait_all(bar(L::kBarP + (j & 1)), (j >> 1) & 1) &&
            wait_all(bar(L::kBarVF + j % L::kVSt), (j / L::kVSt) & 1);
       if (!ok) break;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t vst = sV + (j % L::kVSt) * kKVBytes;
+        const uint64_t vd = vmajor + ((sV + (j % L::kVSt) * kKVBytes) >> 4);
         const bool acc = !((fresh >> (j & 1)) & 1u);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
           pf::umma_bf16_ts(tmem + kOCol, tmem + (j & 1) * kKeys + kk * 8,
-                           sdesc(vst + kk * 16 * 128, kKVSlab, 1024), kIdescPV, acc || kk > 0);
+                           vd + kk * 128, kIdescPV | (QUANT ? 0 : kBf16),
+                           acc || kk > 0);
         umma_commit(bar(L::kBarO + (j & 1)));
         umma_commit(bar(L::kBarVE + j % L::kVSt));
       }
       __syncwarp();
-      if (j + 1 == g) break;  // no tile behind this one
     }
     if (lane == 0) {
       // every product of the CTA completes before tensor memory is released
@@ -747,15 +786,21 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     __syncwarp();
   } else if (QUANT && warp >= kConvWarp) {
     // ------------------------------ converters ------------------------------
-    // The first kConvWarps warps turn K tiles, the others V tiles, sharing a tile's rows. A lane
-    // takes 16 codes at a time: value = the E4M3 code's value or code - zero, exact in bf16,
-    // stored where TMA would put bf16 (128-byte rows of 64 channels, 16-byte chunks XORed with
-    // row % 8). V rows that cannot be read or lie behind the context become zero, and so do
-    // NaN codes of drafts: P is zero for rows that do not see them, but 0 * NaN is not (rows
-    // that see one get it back at the end).
+    // The first kConvWarps warps turn K tiles (and Q), the others V tiles, sharing a tile's rows.
+    // A lane takes 16 codes at a time: value = the E4M3 code's value or code - zero, exact in
+    // f16, stored where TMA would put a 16-bit type (128-byte rows of 64 channels, 16-byte
+    // chunks XORed with row % 8). V rows that cannot be read or lie behind the context become
+    // zero, and so do NaN codes of drafts: P is zero for rows that do not see them, but 0 * NaN
+    // is not (rows that see one get it back at the end).
     const int kv = (warp - kConvWarp) / kConvWarps, sub = (warp - kConvWarp) % kConvWarps;
     const int nst = kv ? L::kVSt : L::kKSt, nst8 = kv ? L::kV8St : L::kK8St;
-    int par = 1;
+    constexpr int kIts = kKeys / 4 / kConvWarps;   // 4 keys an iteration
+    // rows 4 (sub + kConvWarps i) + lane / 8: their low three bits do not change with i
+    static_assert(kConvWarps == 2, "a warp's keys repeat modulo 8");
+    const int q8 = lane & 7, key0 = sub * 4 + (lane >> 3), c0 = 2 * (q8 & 3);
+    const uint32_t at0 = (q8 >> 2) * kKVSlab + key0 * 128 + ((c0 ^ (key0 & 7)) << 4);
+    const uint32_t at1 = (q8 >> 2) * kKVSlab + key0 * 128 + (((c0 + 1) ^ (key0 & 7)) << 4);
+    int pieces = 0, ctx = 0, base = 0;
 #pragma unroll 1
     for (int g = 0;; ++g) {
       const int st = g % nst, st8 = g % nst8;
@@ -764,54 +809,112 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       const TileInfo& ti = info[g % kInfo];
       const int flags = ti.flags;
       if (flags & kEnd) break;
-      if (flags & kFirst) par ^= 1;
+      if (flags & kFirst) {
+        ctx = ti.ctx;
+        base = ti.base;
+        if (!kv) {
+          // Q of the piece: 16 lanes to a row of 128 channels, in place
+          const int qb = q_bufs == 2 ? pieces & 1 : 0;
+          ok = wait_all(bar(L::kBarQF + qb), (q_bufs == 2 ? pieces >> 1 : pieces) & 1);
+          if (!ok) break;
+          float* down = reinterpret_cast<float*>(smem + L::kOffDown) + (pieces & 3) * kRows;
+          const int rows = ti.rows * G;
+#pragma unroll 1
+          for (int r = sub * 2 + (lane >> 4); r < ((rows + 3) & ~3); r += 2 * kConvWarps) {
+            const int ch = lane & 15;
+            const uint32_t at = sQ + (2 * qb + (ch >> 3)) * q_rows * 128 + r * 128 +
+                                (((ch & 7) ^ (r & 7)) << 4);
+            uint32_t x[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const int eb = (int)((__float_as_uint(amax) >> 23) & 0xff);
+            // 2^e puts the row's largest element into [2^14, 2^15)
+            const int e = eb == 0 || eb == 0xff ? 0 : max(-100, min(100, 14 - (eb - 127)));
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = pack_f16x2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+            if (ch == 0) down[r] = __uint_as_float((uint32_t)(127 - e) << 23);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(bar(L::kBarQR + (pieces & 3)));
+        }
+        ++pieces;
+      }
       ok = wait_all(bar((kv ? L::kBarV8F : L::kBarK8F) + st8), (g / nst8) & 1);
       if (ok && g >= nst) ok = wait_all(bar((kv ? L::kBarVE : L::kBarKE) + st), ((g / nst) - 1) & 1);
       if (!ok) break;
-      const uint8_t* src = smem + (kv ? L::kOffV8 : L::kOffK8) + st8 * kCodeBytes;
+      const uint8_t* src = smem + (kv ? L::kOffV8 : L::kOffK8) + st8 * kCodeBytes + key0 * 128 + q8 * 16;
       const uint32_t dst = (kv ? sV : sK) + st * kKVBytes;
-      const int live = ti.ctx - ti.key0, draft0 = ti.base - ti.key0;
-      const uint32_t bad = ti.bad;
-      const int q8 = lane & 7, c0 = 2 * (q8 & 3);
-#pragma unroll 2
-      for (int it = sub; it < kKeys * 8 / 32; it += kConvWarps) {
-        const int key = it * 4 + (lane >> 3);
-        const uint4 raw = *reinterpret_cast<const uint4*>(src + key * 128 + q8 * 16);
-        const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
-        const uint32_t row = dst + (q8 >> 2) * kKVSlab + key * 128;
-        uint32_t o[8];
-        uint32_t nan = 0;
-        const bool gone = kv && (key >= live || ((bad >> (key / BS)) & 1u));
-        if constexpr (KV == PA_INT8) {
-          const float z = 8388736.f + (float)(kv ? ti.vz[key / BS] : ti.kz[key / BS]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) i8x4_to_bf16(wd[k], z, o[2 * k], o[2 * k + 1]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            nan |= ((wd[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            e4m3x4_to_bf16(wd[k], o[2 * k], o[2 * k + 1]);
-          }
-        }
-        if (gone) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = 0;
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     ::"r"(row + ((c0 ^ (key & 7)) << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
-                       "r"(o[3]) : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     ::"r"(row + (((c0 + 1) ^ (key & 7)) << 4)), "r"(o[4]), "r"(o[5]),
-                       "r"(o[6]), "r"(o[7]) : "memory");
-        if (KV == PA_FP8_E4M3 && nan != 0 && !gone) {
-          const bool draft = kv && key >= draft0;
 #pragma unroll 1
-          for (int e = 0; e < 16; ++e)
-            if ((src[key * 128 + q8 * 16 + e] & 0x7f) == 0x7f)
-              asm volatile("st.shared.b16 [%0], %1;"
-                           ::"r"(row + (((c0 + (e >> 3)) ^ (key & 7)) << 4) + (e & 7) * 2),
-                             "h"((uint16_t)(draft ? 0 : 0x7fc0)) : "memory");
-          if (draft) {
+      for (int h = 0; h < 2; ++h) {
+        uint4 raw[kIts / 2];   // loads first: the stores below are ordered among themselves
+#pragma unroll
+        for (int i = 0; i < kIts / 2; ++i)
+          raw[i] = *reinterpret_cast<const uint4*>(src + (h * (kIts / 2) + i) * kConvWarps * 512);
+#pragma unroll
+        for (int i = 0; i < kIts / 2; ++i) {
+          const int step = (h * (kIts / 2) + i) * kConvWarps;
+          const uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t o[8];
+          if constexpr (KV == PA_INT8) {
+            const int b = (key0 + step * 4) / BS;
+            const float z = 1152.f + (float)(kv ? ti.vz[b] : ti.kz[b]);
+            const uint32_t zc = pack_f16x2(z, z);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t u = wd[k] ^ 0x80808080u;
+              o[2 * k] = tc::i8x2_to_f16x2(u, 0x4140, zc);
+              o[2 * k + 1] = tc::i8x2_to_f16x2(u, 0x4342, zc);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[2 * k] = e4m3x2_to_f16x2((uint16_t)(wd[k] & 0xffffu));
+              o[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(wd[k] >> 16));
+            }
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       ::"r"(dst + at0 + step * 512), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       ::"r"(dst + at1 + step * 512), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                       : "memory");
+        }
+      }
+      const int live = ctx - ti.key0, draft0 = base - ti.key0;
+      const uint32_t bad = ti.bad;
+      if (kv && (live < kKeys || bad != 0 || (KV == PA_FP8_E4M3 && draft0 < kKeys))) {
+        const int par = (pieces - 1) & 1;
+#pragma unroll 1
+        for (int i = 0; i < kIts; ++i) {
+          const int step = i * kConvWarps, key = key0 + step * 4;
+          const bool gone = key >= live || ((bad >> (key / BS)) & 1u);
+          if (gone) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
+                           ::"r"(dst + (k ? at1 : at0) + step * 512), "r"(0) : "memory");
+          } else if (KV == PA_FP8_E4M3 && key >= draft0) {
+            const uint4 w = *reinterpret_cast<const uint4*>(src + step * 512);
+            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+            uint32_t nan = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) nan |= (wd[k] & 0x7f7f7f7fu) + 0x01010101u;
+            if (!(nan & 0x80808080u)) continue;
+#pragma unroll 1
+            for (int e = 0; e < 16; ++e)
+              if ((src[step * 512 + e] & 0x7f) == 0x7f)
+                asm volatile("st.shared.b16 [%0], %1;"
+                             ::"r"(dst + (e < 8 ? at0 : at1) + step * 512 + (e & 7) * 2),
+                               "h"((uint16_t)0) : "memory");
             const int j = key - draft0;
             atomicOr(&s_odd[par * 8 + (j >> 5)], 1u << (j & 31));
             any_odd[par] = 1;
@@ -827,10 +930,14 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     const int r = tid;                                 // row of the tile = tensor-memory lane
     const int tok = r / G, head = r - tok * G;
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    const float sl2 = a.scale_log2;
-    int par = 1;
+    float sl2 = a.scale_log2;
+    int par = 1, pieces = 0;
     uint32_t syncs = 0;
     float m_used = -INFINITY, l = 0.f;
+    int base = 0, ctx = 0, rows = 0, kvh = 0, seq = 0, slot = 0;   // of the piece
+    int64_t row = 0;    // this thread's token row
+    bool live_warp = false;
+    float vref = 1.f;   // fp8 / int8: the power of two that P's V scales are relative to
     // the four warps meet, within a bound (one of them may have given up)
     auto meet = [&]() {
       mbar_arrive(bar(L::kBarSm));
@@ -847,15 +954,41 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         m_used = -INFINITY;
         l = 0.f;
         par ^= 1;
+        base = ti.base;
+        ctx = ti.ctx;
+        rows = ti.rows;
+        kvh = ti.kvh;
+        seq = ti.s;
+        slot = ti.slot;
+        row = ti.row0 + min(tok, rows - 1);
+        live_warp = warp * 32 < rows * G;
+        if constexpr (QUANT) {
+          vref = 0.f;
+          ok = wait_all(bar(L::kBarQR + (pieces & 3)), (pieces >> 2) & 1);
+          if (!ok) break;
+          sl2 = a.scale_log2 * reinterpret_cast<const float*>(smem + L::kOffDown)[(pieces & 3) * kRows + r];
+          ++pieces;
+        }
       }
-      const bool live_warp = warp * 32 < ti.rows * G;
-      const int64_t row = ti.row0 + min(tok, ti.rows - 1);
+      float beta = 1.f;
+      if constexpr (QUANT) {
+        float vmax = ti.vs[0];
+#pragma unroll
+        for (int b = 1; b < NB; ++b) vmax = fmaxf(vmax, ti.vs[b]);
+        if (!(vmax <= vref)) {
+          // the next power of two, within a range whose reciprocal is one too
+          const int e = max(27, min(227, (int)((__float_as_uint(vmax) >> 23) & 0xff) + 1));
+          const float up = __uint_as_float((uint32_t)e << 23);
+          beta = vref > 0.f ? fminf(vref / up, 1.f) : 1.f;
+          vref = fmaxf(vref, up);
+        }
+      }
       const uint32_t bad = ti.bad;
-      const int base = ti.base, live = ti.ctx - ti.key0, draft0 = base - ti.key0;
+      const int key0 = ti.key0, live = ctx - key0, draft0 = base - key0;
       const bool masked = draft0 < kKeys || bad != 0;
       uint64_t view = ~0ull;
       if (masked && live_warp) {
-        view = tile_view(a, row, ti.key0, base, ti.ctx);
+        view = tile_view(a, row, key0, base, ctx);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
           if ((bad >> b) & 1u) view &= ~(((1ull << BS) - 1ull) << (b * BS));
@@ -865,9 +998,10 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       tc_fence_after();
       if (live_warp) {
         const uint32_t sbuf = lanes + (g & 1) * kKeys;
+        const float rvs = vref > 0.f ? 128.f / vref : 0.f;   // 0: every V scale so far is
         const float alpha =
-            masked ? softmax_tile<BS, QUANT, true>(sbuf, ti, sl2, view, m_used, l)
-                   : softmax_tile<BS, QUANT, false>(sbuf, ti, sl2, view, m_used, l);
+            beta * (masked ? softmax_tile<BS, QUANT, true>(sbuf, ti, sl2, rvs, view, m_used, l)
+                           : softmax_tile<BS, QUANT, false>(sbuf, ti, sl2, rvs, view, m_used, l));
         if (!(flags & kFirst) && __any_sync(0xffffffffu, alpha != 1.f)) {
           // O holds the tiles before this one once their last product is done
           ok = wait_all(bar(L::kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
@@ -928,11 +1062,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       if (!(flags & kLast)) continue;
 
       // ---- the piece is done: O / l, or the partial ----
-      // what the slot says is read before the slot can be reused (the wait below ends after
-      // this tile's product, several tiles before that)
-      const int rows = ti.rows, kvh = ti.kvh, seq = ti.s, ctx = ti.ctx;
-      const int64_t slot = ti.slot;
-      const bool has_drafts = ti.key0 + kKeys > base;
+      const bool has_drafts = key0 + kKeys > base;
       const bool live_row = tok < rows, whole = (flags & kWhole) != 0;
       ok = wait_all(bar(L::kBarO + (g & 1)), (g >> 1) & 1);
       if (!ok) break;
@@ -947,8 +1077,9 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       }
       const int64_t orow = row * a.num_q_heads + kvh * G + head;
       uint16_t* op = static_cast<uint16_t*>(a.out) + orow * kDim;
-      float4* ap = reinterpret_cast<float4*>(ws.acc) + slot * (kDim / 4) * kRows + r;
-      const float inv = l != 0.f ? 1.f / l : 0.f;
+      float4* ap = reinterpret_cast<float4*>(ws.acc) + (int64_t)slot * (kDim / 4) * kRows + r;
+      const float unit = QUANT ? vref * (1.f / 128.f) : 1.f;
+      const float inv = l != 0.f ? unit / l : 0.f;
       if (live_warp) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -969,8 +1100,8 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               ap[(c * 8 + k) * kRows] =
-                  make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                              __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                  make_float4(__uint_as_float(o[4 * k]) * unit, __uint_as_float(o[4 * k + 1]) * unit,
+                              __uint_as_float(o[4 * k + 2]) * unit, __uint_as_float(o[4 * k + 3]) * unit);
           }
           __syncwarp();
         }
@@ -1036,9 +1167,13 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
 
 // Joins the pieces of every (row tile, sequence, kv head) that a cut falls into: grid (cuts,
 // 4 x 32 rows). The cut where it is first cut does the work; thread (warp w, lane) takes row
-// lane of the group and channels 32 w .. 32 w + 31, pieces in order. Few cuts (at most
-// kStreams - 1), so it is bound by two dependent reads per piece.
-__global__ void __launch_bounds__(128) tree_tc_reduce_kernel(const TreeArgs a, const Workspace ws) {
+// lane of the group and channels 8 w .. 8 w + 7, pieces in order, eight pieces' reads in
+// flight (a context of 20000 tokens in a small batch has two dozen). Bound by latency: two
+// dependent reads and a round trip per eight pieces.
+constexpr int kReduceThreads = 512;
+
+__global__ void __launch_bounds__(kReduceThreads) tree_tc_reduce_kernel(const TreeArgs a,
+                                                                        const Workspace ws) {
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x + 1;
@@ -1053,41 +1188,30 @@ __global__ void __launch_bounds__(128) tree_tc_reduce_kernel(const TreeArgs a, c
   const int rows = min(TM, n - run.rt * TM) * G;
   const int r = 32 * blockIdx.y + (threadIdx.x & 31), w = threadIdx.x >> 5;
   if (r >= rows) return;
-  auto slot_of = [&](int k) {
-    return (int64_t)k * 2 + (k == first && run.begin > run.per * first ? 1 : 0);
-  };
+  // a pair that begins inside run `first` is its last piece, one that begins it its first
+  const int64_t slot0 = (int64_t)first * 2 + (run.begin > run.per * first ? 1 : 0);
+  auto slot_of = [&](int k) { return k == first ? slot0 : (int64_t)k * 2; };
   float M = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = first; k <= last; ++k) M = fmaxf(M, ws.m[slot_of(k) * kRows + r]);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  float4 acc[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 8
   for (int k = first; k <= last; ++k) {
     const int64_t slot = slot_of(k);
+    const float4* src = reinterpret_cast<const float4*>(ws.acc) + (slot * (kDim / 4) + 2 * w) * kRows + r;
+    const float4 u = src[0], v = src[kRows];
     const float f = fast_exp2(ws.m[slot * kRows + r] - ref);
     L = fmaf(f, ws.l[slot * kRows + r], L);
-    const float4* src = reinterpret_cast<const float4*>(ws.acc) + (slot * (kDim / 4) + 8 * w) * kRows + r;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 v = src[j * kRows];
-      acc[j].x = fmaf(f, v.x, acc[j].x);
-      acc[j].y = fmaf(f, v.y, acc[j].y);
-      acc[j].z = fmaf(f, v.z, acc[j].z);
-      acc[j].w = fmaf(f, v.w, acc[j].w);
-    }
+    x.x = fmaf(f, u.x, x.x); x.y = fmaf(f, u.y, x.y); x.z = fmaf(f, u.z, x.z); x.w = fmaf(f, u.w, x.w);
+    y.x = fmaf(f, v.x, y.x); y.y = fmaf(f, v.y, y.y); y.z = fmaf(f, v.z, y.z); y.w = fmaf(f, v.w, y.w);
   }
   const float inv = L != 0.f ? 1.f / L : 0.f;
   const int64_t row = (int64_t)(q0 + run.rt * TM + r / G) * a.num_q_heads + run.kvh * G + r % G;
-  uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * kDim + 32 * w);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 x = acc[2 * j], y = acc[2 * j + 1];
-    op[j] = make_uint4(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv),
-                       pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * kDim + 8 * w) =
+      make_uint4(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv),
+                 pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
   if (w == 0 && a.lse_out != nullptr)
     a.lse_out[row] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
@@ -1125,7 +1249,8 @@ inline cudaError_t launch_bs(const TreeArgs& a, const Workspace& ws, cudaStream_
   e = launch_pdl(tree_tc_kernel<BS, KV>, dim3(kStreams), dim3(L::kThreads), L::kSmem, st, a, ws,
                  qm, km, vm);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_tc_reduce_kernel, dim3(kStreams - 1, kRows / 32), dim3(128), 0, st, a, ws);
+  return launch_pdl(tree_tc_reduce_kernel, dim3(kStreams - 1, kRows / 32),
+                    dim3(kReduceThreads), 0, st, a, ws);
 }
 
 inline cudaError_t launch_tc(const TreeArgs& a, pa_dtype kv, const Workspace& ws, cudaStream_t st) {

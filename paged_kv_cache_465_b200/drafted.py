@@ -42,12 +42,13 @@ def _launch(fn, what: str, dev: int, stream, args) -> None:
     stream as its last argument."""
     torch = _torch()
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        # the handle alone: a Stream object would cost more than the launch's other checks
+        handle = torch._C._cuda_getCurrentRawStream(dev)
     elif stream.device.index != dev:
         raise ValueError("stream belongs to another device than the tensors")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -66,13 +67,16 @@ def _device(x, name) -> int:
 def _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev):
     """(cache dtype code, pointers of the pools, pointers of scales and zero points)."""
     torch = _torch()
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must be alike, [num_blocks, num_kv_heads, B, d]")
-    bh, f32, i32 = k_cache.shape[:2], torch.float32, torch.int32
-    side = (_opt(k_scales, "k_scales", f32, dev, bh), _opt(v_scales, "v_scales", f32, dev, bh),
-            _opt(k_zeros, "k_zeros", i32, dev, bh), _opt(v_zeros, "v_zeros", i32, dev, bh))
-    return _dtype_code(k_cache.dtype), (_ptr(k_cache, "k_cache", k_cache.dtype, dev),
-                                        _ptr(v_cache, "v_cache", k_cache.dtype, dev)), side
+    shape, dt = k_cache.shape, k_cache.dtype
+    if len(shape) != 4:
+        raise ValueError("the caches must be [num_blocks, num_kv_heads, B, d]")
+    pools = _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev, shape)
+    if k_scales is v_scales is k_zeros is v_zeros is None:
+        return _dtype_code(dt), pools, (None, None, None, None)
+    bh, f32, i32 = shape[:2], torch.float32, torch.int32
+    return _dtype_code(dt), pools, (
+        _opt(k_scales, "k_scales", f32, dev, bh), _opt(v_scales, "v_scales", f32, dev, bh),
+        _opt(k_zeros, "k_zeros", i32, dev, bh), _opt(v_zeros, "v_zeros", i32, dev, bh))
 
 
 def build_step(context_lens, new_lens, blocks_held, block_tables, free_blocks, queue_state, *,
@@ -139,15 +143,15 @@ def release_blocks(keep_lens, blocks_held, block_tables, free_blocks, queue_stat
     _launch(_lib.paged_release_blocks, "paged_release_blocks", dev, stream, args)
 
 
-def _rows(x, name, dtype, dev):
+def _rows(x, name, dtype, dev, T, d):
     """(pointer, token stride) of rows [T, heads, d] that may be strided along T."""
-    T, heads, d = x.shape
-    st = x.stride()
+    s0, s1, s2 = x.stride()
     if x.get_device() != dev or x.dtype is not dtype:
         _refuse(x, name, dtype, dev, None)
-    if st[2] != 1 or (heads > 1 and st[1] != d):
+    heads = x.shape[1]
+    if s2 != 1 or (s1 != d and heads > 1):
         raise ValueError(f"{name} rows must be contiguous [heads, d]")
-    return x.data_ptr(), st[0] if T > 1 else heads * d  # a single row has no stride of its own
+    return x.data_ptr(), s0 if T > 1 else heads * d  # a single row has no stride of its own
 
 
 def rotary_and_cache(q, k, v, q_out, k_cache, v_cache, positions, slot_mapping, inv_freq, *,
@@ -175,8 +179,8 @@ def rotary_and_cache(q, k, v, q_out, k_cache, v_cache, positions, slot_mapping, 
         raise ValueError("positions must be [T], or [axes, T] with a section for each of 1 to 4 axes")
     code, pools, side = _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev)
     dt = q.dtype
-    (qp, qs), (kp, ks) = _rows(q, "q", dt, dev), _rows(k, "k", dt, dev)
-    (vp, vs), (op, os_) = _rows(v, "v", dt, dev), _rows(q_out, "q_out", dt, dev)
+    (qp, qs), (kp, ks) = _rows(q, "q", dt, dev, T, d), _rows(k, "k", dt, dev, T, d)
+    (vp, vs), (op, os_) = _rows(v, "v", dt, dev, T, d), _rows(q_out, "q_out", dt, dev, T, d)
     desc = pa_rotary_desc(T, Hq, Hkv, d, 2 * half, axes, sec, adjacent_pairs, B, NB, qs, ks, vs,
                           os_, _dtype_code(dt), code)
     _launch(_lib.rotary_and_cache, "rotary_and_cache", dev, stream, (
