@@ -22,19 +22,31 @@ def _refuse(x, name, dtype, dev, shape):
         raise TypeError(f"{name} has dtype {x.dtype}, expected {dtype}")
     if shape is not None and x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous (its rows, where they may be strided)")
 
 
-def _ptr(x, name, dtype, dev, shape=None):
-    """Device pointer of a contiguous tensor of this type (and shape) on device ``dev``."""
-    if x.get_device() != dev or x.dtype is not dtype or not x.is_contiguous() or \
-            (shape is not None and x.shape != shape):
-        _refuse(x, name, dtype, dev, shape)
-    return x.data_ptr()
+# Replaced by the native helper's functions on their first call: it needs torch, which this
+# package does not import before it is given a tensor.
+def _ptrs(*args):
+    """(dev, tensor, name, dtype, shape, ...) -> device pointers; a tensor may be None, and a
+    shape (any)."""
+    _load_helper()
+    return _ptrs(*args)
 
 
-def _opt(x, name, dtype, dev, shape=None):
-    return None if x is None else _ptr(x, name, dtype, dev, shape)
+def _rows(*args):
+    """(dev, tensor, name, dtype, shape) -> (device pointer, stride) of rows [T, heads, d] that
+    may be strided along T."""
+    _load_helper()
+    return _rows(*args)
+
+
+def _load_helper() -> None:
+    global _ptrs, _rows
+    _torch()
+    from . import _tensors
+    _tensors.on_refusal(_refuse)
+    _ptrs, _rows = _tensors.ptrs, _tensors.rows
 
 
 def _launch(fn, what: str, dev: int, stream, args) -> None:
@@ -65,18 +77,18 @@ def _device(x, name) -> int:
 
 
 def _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev):
-    """(cache dtype code, pointers of the pools, pointers of scales and zero points)."""
+    """(cache dtype code, its shape, pointers of the pools, of scales and zero points)."""
     torch = _torch()
     shape, dt = k_cache.shape, k_cache.dtype
     if len(shape) != 4:
         raise ValueError("the caches must be [num_blocks, num_kv_heads, B, d]")
-    pools = _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev, shape)
+    pools = _ptrs(dev, k_cache, "k_cache", dt, None, v_cache, "v_cache", dt, shape)
     if k_scales is v_scales is k_zeros is v_zeros is None:
-        return _dtype_code(dt), pools, (None, None, None, None)
+        return _dtype_code(dt), shape, pools, (None, None, None, None)
     bh, f32, i32 = shape[:2], torch.float32, torch.int32
-    return _dtype_code(dt), pools, (
-        _opt(k_scales, "k_scales", f32, dev, bh), _opt(v_scales, "v_scales", f32, dev, bh),
-        _opt(k_zeros, "k_zeros", i32, dev, bh), _opt(v_zeros, "v_zeros", i32, dev, bh))
+    return _dtype_code(dt), shape, pools, _ptrs(
+        dev, k_scales, "k_scales", f32, bh, v_scales, "v_scales", f32, bh,
+        k_zeros, "k_zeros", i32, bh, v_zeros, "v_zeros", i32, bh)
 
 
 def build_step(context_lens, new_lens, blocks_held, block_tables, free_blocks, queue_state, *,
@@ -100,25 +112,18 @@ def build_step(context_lens, new_lens, blocks_held, block_tables, free_blocks, q
     i32, dev = torch.int32, _device(context_lens, "context_lens")
     S, rows = context_lens.shape[0], slot_mapping.shape[0]
     words = 0 if tree_mask is None else tree_mask.shape[-1]
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("block_tables must be [S, max_blocks]")
-    args = (
-        _ptr(context_lens, "context_lens", i32, dev, (S,)),
-        _ptr(new_lens, "new_lens", i32, dev, (S,)),
-        _ptr(blocks_held, "blocks_held", i32, dev, (S,)),
-        _opt(parents, "parents", i32, dev, (rows,)),
-        _ptr(block_tables, "block_tables", i32, dev), _ptr(free_blocks, "free_blocks", i32, dev),
-        _ptr(queue_state, "queue_state", i32, dev, (2,)), S, block_tables.shape[1], block_size,
-        num_blocks, free_blocks.numel(), rows, words,
-        _ptr(total_lens, "total_lens", i32, dev, (S,)),
-        _ptr(query_start, "query_start", i32, dev, (S + 1,)),
-        _ptr(blocks_held_out, "blocks_held_out", i32, dev, (S,)),
-        _ptr(queue_state_out, "queue_state_out", i32, dev, (2,)),
-        _ptr(slot_mapping, "slot_mapping", torch.int64, dev, (rows,)),
-        _opt(positions, "positions", i32, dev, (rows,)),
-        _opt(tree_mask, "tree_mask", i32, dev, (rows, words)),
-        _opt(status, "status", i32, dev, (1,)))
-    _launch(_lib.paged_build_step, "paged_build_step", dev, stream, args)
+    width, s1, r1, one, two = block_tables.shape[-1], (S,), (rows,), (1,), (2,)
+    ins = _ptrs(dev, context_lens, "context_lens", i32, s1, new_lens, "new_lens", i32, s1,
+                blocks_held, "blocks_held", i32, s1, parents, "parents", i32, r1,
+                block_tables, "block_tables", i32, (S, width),
+                free_blocks, "free_blocks", i32, None, queue_state, "queue_state", i32, two)
+    outs = _ptrs(dev, total_lens, "total_lens", i32, s1, query_start, "query_start", i32, (S + 1,),
+                 blocks_held_out, "blocks_held_out", i32, s1,
+                 queue_state_out, "queue_state_out", i32, two,
+                 slot_mapping, "slot_mapping", torch.int64, r1, positions, "positions", i32, r1,
+                 tree_mask, "tree_mask", i32, (rows, words), status, "status", i32, one)
+    _launch(_lib.paged_build_step, "paged_build_step", dev, stream, (
+        *ins, S, width, block_size, num_blocks, free_blocks.numel(), rows, words, *outs))
 
 
 def release_blocks(keep_lens, blocks_held, block_tables, free_blocks, queue_state, *,
@@ -129,29 +134,15 @@ def release_blocks(keep_lens, blocks_held, block_tables, free_blocks, queue_stat
     ``build_step``; free_blocks is written."""
     torch = _torch()
     i32, dev = torch.int32, _device(keep_lens, "keep_lens")
-    S = keep_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("block_tables must be [S, max_blocks]")
-    args = (
-        _ptr(keep_lens, "keep_lens", i32, dev, (S,)),
-        _ptr(blocks_held, "blocks_held", i32, dev, (S,)),
-        _ptr(block_tables, "block_tables", i32, dev), _ptr(free_blocks, "free_blocks", i32, dev),
-        _ptr(queue_state, "queue_state", i32, dev, (2,)), S, block_tables.shape[1], block_size,
-        free_blocks.numel(), _ptr(blocks_held_out, "blocks_held_out", i32, dev, (S,)),
-        _ptr(queue_state_out, "queue_state_out", i32, dev, (2,)),
-        _opt(status, "status", i32, dev, (1,)))
-    _launch(_lib.paged_release_blocks, "paged_release_blocks", dev, stream, args)
-
-
-def _rows(x, name, dtype, dev, T, d):
-    """(pointer, token stride) of rows [T, heads, d] that may be strided along T."""
-    s0, s1, s2 = x.stride()
-    if x.get_device() != dev or x.dtype is not dtype:
-        _refuse(x, name, dtype, dev, None)
-    heads = x.shape[1]
-    if s2 != 1 or (s1 != d and heads > 1):
-        raise ValueError(f"{name} rows must be contiguous [heads, d]")
-    return x.data_ptr(), s0 if T > 1 else heads * d  # a single row has no stride of its own
+    S, width = keep_lens.shape[0], block_tables.shape[-1]
+    s1 = (S,)
+    ins = _ptrs(dev, keep_lens, "keep_lens", i32, s1, blocks_held, "blocks_held", i32, s1,
+                block_tables, "block_tables", i32, (S, width),
+                free_blocks, "free_blocks", i32, None, queue_state, "queue_state", i32, (2,))
+    outs = _ptrs(dev, blocks_held_out, "blocks_held_out", i32, s1,
+                 queue_state_out, "queue_state_out", i32, (2,), status, "status", i32, (1,))
+    _launch(_lib.paged_release_blocks, "paged_release_blocks", dev, stream, (
+        *ins, S, width, block_size, free_blocks.numel(), *outs))
 
 
 def rotary_and_cache(q, k, v, q_out, k_cache, v_cache, positions, slot_mapping, inv_freq, *,
@@ -166,28 +157,28 @@ def rotary_and_cache(q, k, v, q_out, k_cache, v_cache, positions, slot_mapping, 
     ``sections`` = frequencies of each axis (time, height, width). A token with a negative
     slot is padding: nothing of it is read or written."""
     torch = _torch()
-    T, Hq, d = q.shape
-    NB, Hkv, B, cd = k_cache.shape
-    dev, half = _device(q, "q"), inv_freq.shape[0]
-    if k.shape != (T, Hkv, d) or v.shape != k.shape or cd != d:
-        raise ValueError("k / v do not match q and the cache")
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must match q")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    qshape, dt, dev = q.shape, q.dtype, _device(q, "q")
+    T, Hq, d = qshape
+    code, (NB, Hkv, B, cd), pools, side = _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros,
+                                                      v_zeros, dev)
+    if cd != d:
+        raise ValueError("head_dim of q and cache differ")
+    half, ps = inv_freq.shape[0], positions.shape
+    axes = 1 if len(ps) == 1 else ps[0]
     sec = (half,) if sections is None else tuple(sections)
-    if positions.dim() > 2 or len(sec) != axes or not 1 <= axes <= 4:
+    if len(ps) > 2 or len(sec) != axes or not 1 <= axes <= 4:
         raise ValueError("positions must be [T], or [axes, T] with a section for each of 1 to 4 axes")
-    code, pools, side = _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev)
-    dt = q.dtype
-    (qp, qs), (kp, ks) = _rows(q, "q", dt, dev, T, d), _rows(k, "k", dt, dev, T, d)
-    (vp, vs), (op, os_) = _rows(v, "v", dt, dev, T, d), _rows(q_out, "q_out", dt, dev, T, d)
+    qp, qs = _rows(dev, q, "q", dt, qshape)
+    op, os_ = _rows(dev, q_out, "q_out", dt, qshape)
+    kp, ks = _rows(dev, k, "k", dt, (T, Hkv, d))
+    vp, vs = _rows(dev, v, "v", dt, (T, Hkv, d))
     desc = pa_rotary_desc(T, Hq, Hkv, d, 2 * half, axes, sec, adjacent_pairs, B, NB, qs, ks, vs,
                           os_, _dtype_code(dt), code)
     _launch(_lib.rotary_and_cache, "rotary_and_cache", dev, stream, (
         qp, kp, vp, op, *pools,
-        _ptr(positions, "positions", torch.int32, dev, (T,) if positions.dim() == 1 else (axes, T)),
-        _ptr(slot_mapping, "slot_mapping", torch.int64, dev, (T,)),
-        _ptr(inv_freq, "inv_freq", torch.float32, dev, (half,)), desc, *side))
+        *_ptrs(dev, positions, "positions", torch.int32, (T,) if len(ps) == 1 else (axes, T),
+               slot_mapping, "slot_mapping", torch.int64, (T,),
+               inv_freq, "inv_freq", torch.float32, (half,)), desc, *side))
 
 
 def _tree_desc(q, k_cache, block_tables) -> pa_decode_desc:
@@ -223,19 +214,20 @@ def paged_attn_tree(q, k_cache, v_cache, block_tables, context_lens, query_start
     torch = _torch()
     dev, i32 = _device(q, "q"), torch.int32
     desc = _tree_desc(q, k_cache, block_tables)
-    T, Hq, _ = q.shape
-    S = desc.num_seqs
-    _, pools, side = _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev)
-    words = tree_mask.shape[-1]
-    args = (
-        _ptr(q, "q", q.dtype, dev), *pools, _ptr(block_tables, "block_tables", i32, dev),
-        _ptr(context_lens, "context_lens", i32, dev, (S,)),
-        _ptr(query_start, "query_start", i32, dev, (S + 1,)),
-        _ptr(tree_mask, "tree_mask", i32, dev, (T, words)), words, T, max_query_len, scale,
-        _ptr(out, "out", q.dtype, dev, q.shape), desc, max_context_len, *side,
-        _opt(lse_out, "lse_out", torch.float32, dev, (T, Hq)),
-        None if workspace is None else _ptr(workspace, "workspace", workspace.dtype, dev),
-        0 if workspace is None else workspace.numel() * workspace.element_size())
+    qshape, dt, S, words = q.shape, q.dtype, desc.num_seqs, tree_mask.shape[-1]
+    T = qshape[0]
+    _, _, pools, side = _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev)
+    (qp, op, bt, cl, qs, mp, lp) = _ptrs(
+        dev, q, "q", dt, None, out, "out", dt, qshape, block_tables, "block_tables", i32, None,
+        context_lens, "context_lens", i32, (S,), query_start, "query_start", i32, (S + 1,),
+        tree_mask, "tree_mask", i32, (T, words),
+        lse_out, "lse_out", torch.float32, qshape[:2])
+    wp, wn = None, 0
+    if workspace is not None:
+        wp, = _ptrs(dev, workspace, "workspace", workspace.dtype, None)
+        wn = workspace.numel() * workspace.element_size()
+    args = (qp, *pools, bt, cl, qs, mp, words, T, max_query_len, scale, op, desc, max_context_len,
+            *side, lp, wp, wn)
     try:
         _launch(_lib.paged_attn_tree, "paged_attn_tree", dev, stream, args)
     except PagedAttnError as e:
@@ -261,18 +253,13 @@ def tree_verify(parents, draft_tokens, target_tokens, query_start, context_lens,
     T, S = parents.shape[0], query_start.shape[0] - 1
     if accepted.dim() != 2:
         raise ValueError("accepted must be [S, max_accept]")
-    A = accepted.shape[1]
-    args = (
-        _ptr(parents, "parents", i32, dev, (T,)),
-        _ptr(draft_tokens, "draft_tokens", i64, dev, (T,)),
-        _ptr(target_tokens, "target_tokens", i64, dev, (T,)),
-        _ptr(query_start, "query_start", i32, dev, (S + 1,)),
-        _ptr(context_lens, "context_lens", i32, dev, (S,)), S, T, A,
-        _ptr(accepted, "accepted", i32, dev, (S, A)),
-        _ptr(num_accepted, "num_accepted", i32, dev, (S,)),
-        _ptr(next_tokens, "next_tokens", i64, dev, (S,)),
-        _ptr(kept_lens, "kept_lens", i32, dev, (S,)))
-    _launch(_lib.tree_verify, "tree_verify", dev, stream, args)
+    A, t1, s1 = accepted.shape[1], (T,), (S,)
+    ins = _ptrs(dev, parents, "parents", i32, t1, draft_tokens, "draft_tokens", i64, t1,
+                target_tokens, "target_tokens", i64, t1, query_start, "query_start", i32, None,
+                context_lens, "context_lens", i32, s1)
+    outs = _ptrs(dev, accepted, "accepted", i32, (S, A), num_accepted, "num_accepted", i32, s1,
+                 next_tokens, "next_tokens", i64, s1, kept_lens, "kept_lens", i32, s1)
+    _launch(_lib.tree_verify, "tree_verify", dev, stream, (*ins, S, T, A, *outs))
 
 
 def compact_accepted(k_cache, v_cache, block_tables, context_lens, query_start, accepted,
@@ -282,15 +269,13 @@ def compact_accepted(k_cache, v_cache, block_tables, context_lens, query_start, 
     (``accepted`` and ``num_accepted`` as ``tree_verify`` gives them)."""
     torch = _torch()
     i32, dev, S = torch.int32, _device(k_cache, "k_cache"), context_lens.shape[0]
-    code, pools, side = _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros, v_zeros, dev)
-    NB, Hkv, B, d = k_cache.shape
-    if accepted.dim() != 2 or block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("accepted must be [S, max_accept] and block_tables [S, max_blocks]")
-    A = accepted.shape[1]
+    code, (NB, Hkv, B, d), pools, side = _cache_ptrs(k_cache, v_cache, k_scales, v_scales, k_zeros,
+                                                     v_zeros, dev)
+    if accepted.dim() != 2:
+        raise ValueError("accepted must be [S, max_accept]")
+    A, width, s1 = accepted.shape[1], block_tables.shape[-1], (S,)
+    ptrs = _ptrs(dev, block_tables, "block_tables", i32, (S, width),
+                 context_lens, "context_lens", i32, s1, query_start, "query_start", i32, (S + 1,),
+                 accepted, "accepted", i32, (S, A), num_accepted, "num_accepted", i32, s1)
     _launch(_lib.compact_accepted, "compact_accepted", dev, stream, (
-        *pools, _ptr(block_tables, "block_tables", i32, dev),
-        _ptr(context_lens, "context_lens", i32, dev, (S,)),
-        _ptr(query_start, "query_start", i32, dev, (S + 1,)),
-        _ptr(accepted, "accepted", i32, dev, (S, A)),
-        _ptr(num_accepted, "num_accepted", i32, dev, (S,)), S, A, block_tables.shape[1], Hkv, d, B,
-        NB, code, *side))
+        *pools, *ptrs, S, A, width, Hkv, d, B, NB, code, *side))
