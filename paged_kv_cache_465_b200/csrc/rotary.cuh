@@ -9,7 +9,7 @@
 //
 // Bound: HBM. Per token it reads q, k, v once and writes q_out and the two cache rows once;
 // the unfused sequence would write k and read it again. Loads are issued before the angles
-// are formed.
+// are formed. A step's few tokens are bound by latency instead (3 us).
 #pragma once
 
 #include "common.cuh"
@@ -97,13 +97,19 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&x)[8], 
   }
 }
 
-constexpr int kThreads = 128;
-constexpr int kBatch = 4;  // 32-byte units a thread has in flight
+// Small CTAs, sixteen to an SM (eight for float32 rows, twice the registers): a token goes
+// through slot, loads, angles, a barrier and stores one after the other, and only other tokens
+// fill those waits. 16384 tokens of 32 + 2 x 8 heads into a bf16 cache take 64 us with 64
+// threads x 3 units x 16 CTAs (6.2 TB/s, 95 % of the measured copy), 68 with 128 x 3 x 8, 81 with
+// 128 x 2 and no bound on registers, 105 with 256 x 2, 130 with one thread for every unit.
+constexpr int kThreads = 64;
+constexpr int kBatch = 3;  // 32-byte units a thread has in flight
 
 // A unit is 16 channels of one head: the two 8-channel chunks that turn together (half-split
 // pairs: 8u.. and R / 2 + 8u..), or two neighbouring chunks.
 template <pa_dtype IN, pa_dtype CACHE>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, IN == PA_F32 ? 8 : 16)
+rotary_kernel(const RotaryArgs a) {
   __shared__ float s_cos[128], s_sin[128];
   pdl_wait();
   pdl_trigger();
@@ -117,9 +123,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   const int64_t blk = slot / a.block_size;
   const int off = (int)(slot - blk * a.block_size);
   const int D = a.head_dim, half = a.rotary_dim / 2;
-  const int per_head = D / 16, turning = a.rotary_dim / 16;
-  const int qk = (a.num_q_heads + a.num_kv_heads) * per_head;
-  const int units = qk + a.num_kv_heads * per_head;
+  const int lg = 31 - __clz(D / 16), turning = a.rotary_dim / 16;   // 2^lg units to a head
+  const int qk = (a.num_q_heads + a.num_kv_heads) << lg;
+  const int units = qk + (a.num_kv_heads << lg);
 
   // unit i: head h of all (q, then k, then v), channels c0 .. and c1 .. of it
   struct Unit {
@@ -128,8 +134,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   };
   auto unit = [&](int i) {
     Unit u;
-    u.h = i / per_head;
-    const int r = i - u.h * per_head;
+    u.h = i >> lg;
+    const int r = i - (u.h << lg);
     u.turn = i < qk && r < turning;
     if (u.turn && !a.adjacent) {
       u.c0 = 8 * r;
@@ -169,13 +175,13 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
     }
     if (!angles) {
       angles = true;
-      if (tid < half) {
+      for (int f = tid; f < half; f += kThreads) {
         int axis = 0;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) axis += tid >= a.sec_end[k];
+        for (int k = 0; k < 3; ++k) axis += f >= a.sec_end[k];
         const double turns = (double)a.positions[(int64_t)axis * a.num_tokens + t] *
-                             (double)a.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
-        sincospif(2.f * (float)(turns - rint(turns)), &s_sin[tid], &s_cos[tid]);
+                             (double)a.inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
+        sincospif(2.f * (float)(turns - rint(turns)), &s_sin[f], &s_cos[f]);
       }
       __syncthreads();
     }
