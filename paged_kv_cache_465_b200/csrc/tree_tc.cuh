@@ -441,7 +441,13 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  if (warp == 0) {
+    pf::tmem_alloc(smem_u32(tmem_slot), kCols);
+    pf::tmem_relinquish();
+  }
   pdl_wait();
+  // the joining launch may take its place on idle SMs now; it waits for this grid's end
+  pdl_trigger();
   // ---- the batch's key tiles, and where this CTA's run begins ----
   const int rts = row_tiles_of(a.max_query_len, G);
   const int seqs_per = (a.num_seqs + kThreads - 1) / kThreads;
@@ -453,24 +459,28 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     else if (blockIdx.x == 0) flag_error(PA_DEVERR_QUERY);
   }
   int64_t total;
-  scan1<W>(mine, total, s_scan);
+  const int64_t before = scan1<W>(mine, total, s_scan);
+  const int64_t seq_total = total;
   total *= Hkv;
   const int64_t per = (total + kStreams - 1) / kStreams;
   const int64_t w0 = per * blockIdx.x, count = min(per, total - w0);
   if (count <= 0) {
     if (tid == 0) ws.runs[blockIdx.x].tiles = 0;
+    if (warp == 0) pf::tmem_dealloc(*tmem_slot, kCols);   // its own warp's allocation
     return;
   }
   int64_t done = 0;
 #pragma unroll 1
   for (int rt = 0; rt < rts; ++rt) {
-    int64_t sum = 0;
-    for (int s = s0; s < s1; ++s) {
-      int q0, n, ctx;
-      if (seq_range(a, s, q0, n, ctx) && row_tiles_of(n, G) > rt) sum += tiles_of(ctx) + kPieceCost;
+    int64_t sum = mine, all = seq_total, at = before;   // all there is with one row tile
+    if (rts > 1) {
+      sum = 0;
+      for (int s = s0; s < s1; ++s) {
+        int q0, n, ctx;
+        if (seq_range(a, s, q0, n, ctx) && row_tiles_of(n, G) > rt) sum += tiles_of(ctx) + kPieceCost;
+      }
+      at = scan1<W>(sum, all, s_scan);
     }
-    int64_t all;
-    int64_t at = scan1<W>(sum, all, s_scan);
     if (w0 < done + all * Hkv) {
       at = done + at * Hkv;
       if (w0 >= at && w0 < at + sum * Hkv) {  // one thread's sequences hold it
@@ -493,10 +503,6 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       break;
     }
     done += all * Hkv;
-  }
-  if (warp == 0) {
-    pf::tmem_alloc(smem_u32(tmem_slot), kCols);
-    pf::tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
@@ -538,6 +544,13 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         w.any = more;
       }
       const bool want = more && lane < n * NB && blk * BS < pc.ctx;
+      if (more && first) {
+        // the rows' masks into L1: the softmax reads them when the piece begins
+        const int toks = min(TM, pc.n - pc.rt * TM);
+        const uint32_t* m = a.tree_mask + (int64_t)(pc.q0 + pc.rt * TM) * a.mask_words;
+        for (int i = lane * 32; i < toks * a.mask_words; i += 1024)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(m + i) : "memory");
+      }
       copy4(&w.id[lane], a.block_tables + (want ? (int64_t)pc.s * a.max_blocks_per_seq + blk : 0), want);
       wt += n;
     };
@@ -1158,7 +1171,6 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
   // ------------------------------ teardown ------------------------------
   tc_fence_before();
   __syncthreads();
-  pdl_trigger();
   if (warp == 0) {
     tc_fence_after();
     pf::tmem_dealloc(tmem, kCols);
