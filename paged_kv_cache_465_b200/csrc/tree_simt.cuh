@@ -33,6 +33,7 @@ struct TreeArgs {
   int num_seqs, num_tokens, num_q_heads, num_kv_heads, group;
   int max_blocks_per_seq, num_blocks, block_size, mask_words;
   int max_context_len, max_query_len;
+  int q_rows;                   // tensor-core path: rows of a Q tile in shared memory
   pa_dtype q_dtype, out_dtype;
   // CUDA-core path: parts of the context
   float* part_m;                // [T][Hq][parts]

@@ -81,7 +81,8 @@ constexpr int kStreams = 296;              // runs the batch is cut into: two CT
 constexpr int kPieceCost = PA_TREE_PIECE_COST;
 constexpr int kMmaWarp = 4, kTmaWarp = 5, kConvWarp = 6;
 constexpr int kConvWarps = 2;              // converter warps for K, and as many for V
-constexpr int kQBytes = 2 * kRows * 128;   // Q: one tile of 128 rows, or two of up to 64
+constexpr int kQBytes = 2 * kRows * 128;   // Q: one tile of 128 rows, or smaller ones
+constexpr int kCodeSt = 3;                 // staged codes: a ring of tiles, K and V in turn
 constexpr int kKVSlab = kKeys * 128;       // 64 channels x 64 keys
 constexpr int kKVBytes = 2 * kKVSlab;
 constexpr int kCodeBytes = kKeys * 128;    // one-byte codes of 64 keys
@@ -126,31 +127,28 @@ constexpr int kWindows = 4;
 template <bool QUANT>
 struct Layout {
   static constexpr int kThreads = QUANT ? 192 + 64 * kConvWarps : 192;
-  static constexpr int kKSt = QUANT ? 1 : 2;     // bf16 tiles of K and of V
-  static constexpr int kVSt = QUANT ? 1 : 2;
-  static constexpr int kK8St = QUANT ? 3 : 0;    // staged codes
-  static constexpr int kV8St = QUANT ? 2 : 0;
+  // 16-bit tiles of K and of V: two each, but for codes and 128 rows, whose Q takes the place
+  // of the second K tile (k_st below)
+  static constexpr int kVSt = 2;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kQBytes;
-  static constexpr int kOffV = kOffK + kKSt * kKVBytes;
-  static constexpr int kOffK8 = kOffV + kVSt * kKVBytes;
-  static constexpr int kOffV8 = kOffK8 + kK8St * kCodeBytes;
-  static constexpr int kOffInfo = kOffV8 + kV8St * kCodeBytes;
+  static constexpr int kOffK = QUANT ? kQBytes / 2 : kQBytes;
+  static constexpr int kOffV = kOffK + 2 * kKVBytes;
+  static constexpr int kOffC = kOffV + kVSt * kKVBytes;
+  static constexpr int kOffInfo = kOffC + (QUANT ? kCodeSt * kCodeBytes : 0);
   static constexpr int kOffWin = kOffInfo + kInfo * (int)sizeof(TileInfo);
   static constexpr int kOffMisc = kOffWin + kWindows * (int)sizeof(Window);
   static constexpr int kOffDown = kOffMisc + 384;          // float [4][kRows]: what undoes Q's factors
   static constexpr int kOffBar = kOffDown + (QUANT ? 4 * kRows * 4 : 0);
   // barriers
   static constexpr int kBarQF = 0, kBarQE = 2;   // [2] each
-  static constexpr int kBarKF = 4, kBarKE = kBarKF + kKSt;
-  static constexpr int kBarVF = kBarKE + kKSt, kBarVE = kBarVF + kVSt;
+  static constexpr int kBarKF = 4, kBarKE = kBarKF + 2;
+  static constexpr int kBarVF = kBarKE + 2, kBarVE = kBarVF + kVSt;
   static constexpr int kBarSF = kBarVE + kVSt;   // [2] S in tensor memory
   static constexpr int kBarP = kBarSF + 2;       // [2] P in tensor memory
   static constexpr int kBarO = kBarP + 2;        // [2] P V done
   static constexpr int kBarInfo = kBarO + 2;     // [kInfo]
-  static constexpr int kBarK8F = kBarInfo + kInfo, kBarK8E = kBarK8F + kK8St;
-  static constexpr int kBarV8F = kBarK8E + kK8St, kBarV8E = kBarV8F + kV8St;
-  static constexpr int kBarQR = kBarV8E + kV8St;  // [4] Q converted
+  static constexpr int kBarCF = kBarInfo + kInfo, kBarCE = kBarCF + (QUANT ? kCodeSt : 0);
+  static constexpr int kBarQR = kBarCE + (QUANT ? kCodeSt : 0);  // [4] Q converted
   static constexpr int kBarSm = kBarQR + (QUANT ? 4 : 0);  // the four softmax warps, once a piece
   static constexpr int kBarFin = kBarSm + 1;
   static constexpr int kNumBars = kBarFin + 1;
@@ -406,11 +404,15 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
                                              ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, TM = kRows / G, Hkv = a.num_kv_heads;
-  // a step of up to 64 rows per sequence keeps two pieces' Q (the product still reads 128
-  // rows: what lies behind the 64 gives rows that nobody uses)
-  const int q_rows = a.max_query_len * G <= kRows / 2 ? kRows / 2 : kRows;
-  const int q_bufs = kRows / q_rows;
-  const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK);
+  // A step of few rows per sequence keeps two pieces' Q (the product still reads 128 rows:
+  // what lies behind Q gives rows that nobody uses), or a second K tile.
+  const int q_rows = a.q_rows;
+  const int q_bufs = q_rows == (QUANT ? kRows / 4 : kRows / 2) ? 2 : 1;
+  const int k_st = QUANT && q_rows == kRows ? 1 : 2;
+  auto k_of = [&](int g) { return k_st == 2 ? g & 1 : 0; };         // tile g's K: its stage,
+  auto k_use = [&](int g) { return k_st == 2 ? g >> 1 : g; };       // and which use of it
+  const uint32_t sQ = smem_u32(smem + L::kOffQ);
+  const uint32_t sK = smem_u32(smem + (k_st == 1 ? kQBytes : L::kOffK));
   const uint32_t sV = smem_u32(smem + L::kOffV);
   const uint32_t bar0 = smem_u32(smem + L::kOffBar);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
@@ -418,25 +420,24 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + L::kOffMisc);          // [16]
   int* s_start = reinterpret_cast<int*>(s_scan + 16);                       // rt, s, kvh, place
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_start + 4);
-  // drafts of the current piece whose V row holds a NaN or infinity, by draft index
-  // (two lists, for even and odd pieces: the converters may be one piece ahead)
-  uint32_t* s_odd = reinterpret_cast<uint32_t*>(tmem_slot + 2);              // [2][8]
-  volatile int* any_odd = reinterpret_cast<volatile int*>(s_odd + 16);       // [2]
+  // drafts of the current piece whose V row holds a NaN or infinity, by draft index (a ring
+  // of four lists: the converters may be two pieces ahead of the softmax)
+  uint32_t* s_odd = reinterpret_cast<uint32_t*>(tmem_slot + 2);              // [4][8]
+  volatile int* any_odd = reinterpret_cast<volatile int*>(s_odd + 32);       // [4]
 
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       uint32_t count = 1;
       if (i == L::kBarP || i == L::kBarP + 1 || i == L::kBarSm) count = kRows;
-      if (QUANT && ((i >= L::kBarKF && i < L::kBarKF + L::kKSt) ||
+      if (QUANT && ((i >= L::kBarKF && i < L::kBarKF + 2) ||
                     (i >= L::kBarVF && i < L::kBarVF + L::kVSt) ||
-                    (i >= L::kBarK8E && i < L::kBarK8E + L::kK8St) ||
-                    (i >= L::kBarV8E && i < L::kBarV8E + L::kV8St) ||
+                    (i >= L::kBarCE && i < L::kBarCE + kCodeSt) ||
                     (i >= L::kBarQR && i < L::kBarQR + 4)))
         count = 32 * kConvWarps;
       mbar_init(bar(i), count);
     }
-    for (int i = 0; i < 16; ++i) s_odd[i] = 0;
-    any_odd[0] = any_odd[1] = 0;
+    for (int i = 0; i < 32; ++i) s_odd[i] = 0;
+    for (int i = 0; i < 4; ++i) any_odd[i] = 0;
     s_start[0] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -632,28 +633,32 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         const uint32_t bytes = (uint32_t)__popc((good >> (k * NB)) & ((1u << NB) - 1u)) * BS * 128u;
         const bool my_turn = mine == k && p >= 0;
         TileInfo& ti = info[g % kInfo];
-        // ---- K: the ring's stage is free once its last reader is done ----
-        {
-          constexpr int nst = QUANT ? L::kK8St : L::kKSt;
-          constexpr int full = QUANT ? L::kBarK8F : L::kBarKF, empty = QUANT ? L::kBarK8E : L::kBarKE;
-          const int st = g % nst;
-          if (g >= nst) ok = wait_all(bar(empty + st), ((g / nst) - 1) & 1);
-          if (!ok) break;
+        // K or V of this tile into its ring's stage, free once its last reader is done
+        auto copy = [&](const CUtensorMap* map, int full, int empty, int st, int use, uint32_t dst) {
+          if (use > 0) ok = wait_all(bar(empty + st), (use - 1) & 1);
+          if (!ok) return;
           if (lane == 0) mbar_arrive_tx(bar(full + st), QUANT ? bytes : 2 * bytes);
           __syncwarp();
           if (my_turn) {
             if constexpr (QUANT) {
-              tc::tma_load_2d(smem_u32(smem + L::kOffK8) + st * kCodeBytes + off, &kmap, 0, row,
-                              bar(full + st), keep);
+              tc::tma_load_2d(dst + off, map, 0, row, bar(full + st), keep);
             } else {
-              pf::tma_load_3d(sK + st * kKVBytes + off, &kmap, 0, 0, row, bar(full + st));
-              pf::tma_load_3d(sK + st * kKVBytes + kKVSlab + off, &kmap, 0, 1, row, bar(full + st));
+              pf::tma_load_3d(dst + off, map, 0, 0, row, bar(full + st));
+              pf::tma_load_3d(dst + kKVSlab + off, map, 0, 1, row, bar(full + st));
             }
           }
+        };
+        const uint32_t sC = smem_u32(smem + L::kOffC);
+        int c = 2 * g;   // codes: K and V of a tile follow one another through one ring
+        if constexpr (QUANT) {
+          copy(&kmap, L::kBarCF, L::kBarCE, c % kCodeSt, c / kCodeSt, sC + (c % kCodeSt) * kCodeBytes);
+        } else {
+          copy(&kmap, L::kBarKF, L::kBarKE, k_of(g), k_use(g), sK + k_of(g) * kKVBytes);
         }
-        // The description's slot is free: the stage's K (bf16) or codes (two tiles' conversions
-        // later) could only be read after S(g - 4) at the earliest, which was issued behind
-        // P V (g - 6), so softmax and converters are past tile g - 6 > g - kInfo.
+        if (!ok) break;
+        // The description's slot is free. bf16: K(g - 2) was read by S(g - 2), issued behind
+        // P V (g - 4). Codes: those of V(g - 2) at least are converted, into a tile that
+        // P V (g - 4) had read. So softmax and converters are past tile g - 4 > g - kInfo.
         if (QUANT && mine == k) {
           ti.ks[lane & (NB - 1)] = ks;
           ti.vs[lane & (NB - 1)] = vs;
@@ -679,25 +684,13 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kBarInfo + g % kInfo));
-        // ---- V ----
-        {
-          constexpr int nst = QUANT ? L::kV8St : L::kVSt;
-          constexpr int full = QUANT ? L::kBarV8F : L::kBarVF, empty = QUANT ? L::kBarV8E : L::kBarVE;
-          const int st = g % nst;
-          if (g >= nst) ok = wait_all(bar(empty + st), ((g / nst) - 1) & 1);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_tx(bar(full + st), QUANT ? bytes : 2 * bytes);
-          __syncwarp();
-          if (my_turn) {
-            if constexpr (QUANT) {
-              tc::tma_load_2d(smem_u32(smem + L::kOffV8) + st * kCodeBytes + off, &vmap, 0, row,
-                              bar(full + st), keep);
-            } else {
-              pf::tma_load_3d(sV + st * kKVBytes + off, &vmap, 0, 0, row, bar(full + st));
-              pf::tma_load_3d(sV + st * kKVBytes + kKVSlab + off, &vmap, 0, 1, row, bar(full + st));
-            }
-          }
+        ++c;
+        if constexpr (QUANT) {
+          copy(&vmap, L::kBarCF, L::kBarCE, c % kCodeSt, c / kCodeSt, sC + (c % kCodeSt) * kCodeBytes);
+        } else {
+          copy(&vmap, L::kBarVF, L::kBarVE, g % L::kVSt, g / L::kVSt, sV + (g % L::kVSt) * kKVBytes);
         }
+        if (!ok) break;
       }
       if (!ok) break;
       if (w.tile0 + w.ntiles == w.pc.t1) run_first = false;
@@ -712,12 +705,14 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         // copies in flight complete (each barrier's last phase) before shared memory is released
         for (int i = max(0, pieces - q_bufs); i < pieces; ++i)
           mbar_wait(bar(L::kBarQF + i % q_bufs), (i / q_bufs) & 1);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const int nst = QUANT ? (kv ? L::kV8St : L::kK8St) : (kv ? L::kVSt : L::kKSt);
-          const int full = QUANT ? (kv ? L::kBarV8F : L::kBarK8F) : (kv ? L::kBarVF : L::kBarKF);
-          for (int j = max(0, g - nst); j <= g; ++j)
-            mbar_wait(bar(full + j % nst), (j / nst) & 1);
+        if (QUANT) {
+          for (int c = max(0, 2 * g + 1 - kCodeSt); c <= 2 * g + 1; ++c)
+            mbar_wait(bar(L::kBarCF + c % kCodeSt), (c / kCodeSt) & 1);
+        } else {
+          for (int j = max(0, g - 2); j <= g; ++j) {
+            mbar_wait(bar(L::kBarKF + k_of(j)), k_use(j) & 1);
+            mbar_wait(bar(L::kBarVF + j % L::kVSt), (j / L::kVSt) & 1);
+          }
         }
       }
     }
@@ -745,13 +740,13 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         q_lo = (sQ >> 4) + q_buf * q_rows * 16;
         ++pieces;
       }
-      ok = wait_all(bar(L::kBarKF + g % L::kKSt), (g / L::kKSt) & 1);
+      ok = wait_all(bar(L::kBarKF + k_of(g)), k_use(g) & 1);
       if (!ok) return false;
       tc_fence_after();
       const uint32_t b = 1u << (g & 1);
       fresh = (flags & kFirst) ? fresh | b : fresh & ~b;
       if (lane == 0) {
-        const uint64_t kd = kmajor + ((sK + (g % L::kKSt) * kKVBytes) >> 4);
+        const uint64_t kd = kmajor + ((sK + k_of(g) * kKVBytes) >> 4);
         const uint64_t qd0 = kmajor + q_lo, qd1 = qd0 + q_slab;
 #pragma unroll
         for (int kk = 0; kk < kDim / 16; ++kk)
@@ -759,7 +754,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
                         kd + (kk >> 2) * (kKVSlab / 16) + (kk & 3) * 2,
                         kIdescS | (QUANT ? 0 : kBf16), kk > 0);
         umma_commit(bar(L::kBarSF + (g & 1)));
-        umma_commit(bar(L::kBarKE + g % L::kKSt));
+        umma_commit(bar(L::kBarKE + k_of(g)));
         if (flags & kLast) umma_commit(bar(L::kBarQE + q_buf));
       }
       __syncwarp();
@@ -806,7 +801,6 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     // zero, and so do NaN codes of drafts: P is zero for rows that do not see them, but 0 * NaN
     // is not (rows that see one get it back at the end).
     const int kv = (warp - kConvWarp) / kConvWarps, sub = (warp - kConvWarp) % kConvWarps;
-    const int nst = kv ? L::kVSt : L::kKSt, nst8 = kv ? L::kV8St : L::kK8St;
     constexpr int kIts = kKeys / 4 / kConvWarps;   // 4 keys an iteration
     // rows 4 (sub + kConvWarps i) + lane / 8: their low three bits do not change with i
     static_assert(kConvWarps == 2, "a warp's keys repeat modulo 8");
@@ -816,7 +810,8 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     int pieces = 0, ctx = 0, base = 0;
 #pragma unroll 1
     for (int g = 0;; ++g) {
-      const int st = g % nst, st8 = g % nst8;
+      const int st = kv ? g % L::kVSt : k_of(g), use = kv ? g / L::kVSt : k_use(g);
+      const int c = 2 * g + kv, cst = c % kCodeSt;
       ok = wait_info(g);
       if (!ok) break;
       const TileInfo& ti = info[g % kInfo];
@@ -861,10 +856,10 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         }
         ++pieces;
       }
-      ok = wait_all(bar((kv ? L::kBarV8F : L::kBarK8F) + st8), (g / nst8) & 1);
-      if (ok && g >= nst) ok = wait_all(bar((kv ? L::kBarVE : L::kBarKE) + st), ((g / nst) - 1) & 1);
+      ok = wait_all(bar(L::kBarCF + cst), (c / kCodeSt) & 1);
+      if (ok && use > 0) ok = wait_all(bar((kv ? L::kBarVE : L::kBarKE) + st), (use - 1) & 1);
       if (!ok) break;
-      const uint8_t* src = smem + (kv ? L::kOffV8 : L::kOffK8) + st8 * kCodeBytes + key0 * 128 + q8 * 16;
+      const uint8_t* src = smem + L::kOffC + cst * kCodeBytes + key0 * 128 + q8 * 16;
       const uint32_t dst = (kv ? sV : sK) + st * kKVBytes;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -905,7 +900,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       const int live = ctx - ti.key0, draft0 = base - ti.key0;
       const uint32_t bad = ti.bad;
       if (kv && (live < kKeys || bad != 0 || (KV == PA_FP8_E4M3 && draft0 < kKeys))) {
-        const int par = (pieces - 1) & 1;
+        const int par = (pieces - 1) & 3;
 #pragma unroll 1
         for (int i = 0; i < kIts; ++i) {
           const int step = i * kConvWarps, key = key0 + step * 4;
@@ -935,7 +930,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(bar((kv ? L::kBarV8E : L::kBarK8E) + st8));
+      mbar_arrive(bar(L::kBarCE + cst));
       mbar_arrive(bar((kv ? L::kBarVF : L::kBarKF) + st));
     }
   } else if (warp < 4) {
@@ -944,7 +939,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     const int tok = r / G, head = r - tok * G;
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
     float sl2 = a.scale_log2;
-    int par = 1, pieces = 0;
+    int par = 3, pieces = 0;
     uint32_t syncs = 0;
     float m_used = -INFINITY, l = 0.f;
     int base = 0, ctx = 0, rows = 0, kvh = 0, seq = 0, slot = 0;   // of the piece
@@ -966,7 +961,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       if (flags & kFirst) {
         m_used = -INFINITY;
         l = 0.f;
-        par ^= 1;
+        par = (par + 1) & 3;
         base = ti.base;
         ctx = ti.ctx;
         rows = ti.rows;
@@ -1232,7 +1227,7 @@ __global__ void __launch_bounds__(kReduceThreads) tree_tc_reduce_kernel(const Tr
 inline bool make_q_map(CUtensorMap* m, const TreeArgs& a) {
   auto enc = tc::encoder();
   if (enc == nullptr) return false;
-  const int rows = a.max_query_len * a.group <= kRows / 2 ? kRows / 2 : kRows;
+  const int rows = a.q_rows;
   cuuint64_t dims[4] = {64, 2, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.num_tokens};
   cuuint64_t strides[3] = {128, 256, (cuuint64_t)a.num_q_heads * 256};
   cuuint32_t box[4] = {64, 1, (cuuint32_t)a.group, (cuuint32_t)(rows / a.group)};
@@ -1244,8 +1239,10 @@ inline bool make_q_map(CUtensorMap* m, const TreeArgs& a) {
 }
 
 template <int BS, pa_dtype KV>
-inline cudaError_t launch_bs(const TreeArgs& a, const Workspace& ws, cudaStream_t st) {
+inline cudaError_t launch_bs(TreeArgs a, const Workspace& ws, cudaStream_t st) {
   using L = Layout<KV != PA_BF16>;
+  const int most = a.max_query_len * a.group;   // rows of a sequence and kv head
+  a.q_rows = most > kRows / 2 ? kRows : KV != PA_BF16 && most <= kRows / 4 ? kRows / 4 : kRows / 2;
   CUtensorMap qm, km, vm;
   const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * BS;
   const bool maps = KV == PA_BF16 ? pf::make_kv_map(&km, a.k_cache, rows, BS) &&
