@@ -192,6 +192,15 @@ inline Workspace workspace_at(void* p) {
   return w;
 }
 
+// True in one lane of a converged warp, always the same one. Unlike `lane == 0` it tells the
+// compiler that one thread runs what follows, whose operands then stay in uniform registers.
+__device__ __forceinline__ bool one_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
 // A four-byte asynchronous copy into shared memory, or four zero bytes.
 __device__ __forceinline__ void copy4(void* dst, const void* src, bool go) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
@@ -390,6 +399,45 @@ __device__ __forceinline__ float softmax_tile(uint32_t sbuf, const TileInfo& ti,
   return alpha;
 }
 
+// The same for a tile that every row sees whole, against the reference as it stands, in one
+// pass without the maximum. True when that was right: the weights' sum is below 2^8, so none of
+// them is above it. Otherwise (a score outgrew the reference, or is no number) nothing was
+// written and the two passes above have to be taken. Most tiles end here, with half the
+// instructions: the softmax of few rows is one warp's, and sets the pace.
+template <int BS, bool QUANT>
+__device__ __forceinline__ bool softmax_tile_fast(uint32_t sbuf, const TileInfo& ti, float sl2,
+                                                  float rvs, float m_used, float& l) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t pk[32];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t sv[32];
+    tmem_ld32(sbuf + c * 32, sv);
+    tmem_wait_ld(sv);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float f = QUANT ? sl2 * ti.ks[c * (32 / BS) + e / BS] : sl2;
+      float p0 = fast_exp2(fmaf(__uint_as_float(sv[e]), f, -m_used));
+      float p1 = fast_exp2(fmaf(__uint_as_float(sv[e + 1]), f, -m_used));
+      sum[e & 3] += p0;
+      sum[(e + 1) & 3] += p1;
+      if constexpr (QUANT) {
+        const float vs = ti.vs[c * (32 / BS) + e / BS] * rvs;
+        p0 *= vs;
+        p1 *= vs;
+      }
+      pk[c * 16 + (e >> 1)] = QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+    }
+  }
+  const float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  // one vote: a warp takes one path, its loads and stores are collective
+  if (!__all_sync(0xffffffffu, s <= 256.f)) return false;
+  tmem_st32(sbuf, pk);
+  l += s;
+  tmem_wait_st();
+  return true;
+}
+
 template <int BS, pa_dtype KV>
 __global__ void __launch_bounds__(Layout<KV != PA_BF16>::kThreads, 2)
 tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUtensorMap qmap,
@@ -402,7 +450,8 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform, and known to be
   const int G = a.group, TM = kRows / G, Hkv = a.num_kv_heads;
   // A step of few rows per sequence keeps two pieces' Q (the product still reads 128 rows:
   // what lies behind Q gives rows that nobody uses), or a second K tile.
@@ -508,7 +557,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // waits are made warp-uniform
   auto wait_all = [&](uint32_t b, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(b, parity)) != 0;
@@ -730,7 +779,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
     auto next_s = [&]() {
       ok = wait_info(g);
       if (!ok) return false;
-      const int flags = info[g % kInfo].flags;
+      const int flags = __shfl_sync(0xffffffffu, info[g % kInfo].flags, 0);
       if (flags & kEnd) return false;
       if (flags & kFirst) {
         q_buf = q_bufs == 2 ? pieces & 1 : 0;
@@ -745,7 +794,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       tc_fence_after();
       const uint32_t b = 1u << (g & 1);
       fresh = (flags & kFirst) ? fresh | b : fresh & ~b;
-      if (lane == 0) {
+      if (one_lane()) {
         const uint64_t kd = kmajor + ((sK + k_of(g) * kKVBytes) >> 4);
         const uint64_t qd0 = kmajor + q_lo, qd1 = qd0 + q_slab;
 #pragma unroll
@@ -773,7 +822,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
            wait_all(bar(L::kBarVF + j % L::kVSt), (j / L::kVSt) & 1);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
+      if (one_lane()) {
         const uint64_t vd = vmajor + ((sV + (j % L::kVSt) * kKVBytes) >> 4);
         const bool acc = !((fresh >> (j & 1)) & 1u);
 #pragma unroll
@@ -786,7 +835,7 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       }
       __syncwarp();
     }
-    if (lane == 0) {
+    if (one_lane()) {
       // every product of the CTA completes before tensor memory is released
       umma_commit(bar(L::kBarFin));
       mbar_wait(bar(L::kBarFin), 0);
@@ -1007,10 +1056,12 @@ tree_tc_kernel(const TreeArgs a, const Workspace ws, const __grid_constant__ CUt
       if (live_warp) {
         const uint32_t sbuf = lanes + (g & 1) * kKeys;
         const float rvs = vref > 0.f ? 128.f / vref : 0.f;   // 0: every V scale so far is
-        const float alpha =
+        const bool fast = !masked && !(flags & kFirst) && beta == 1.f &&
+                          softmax_tile_fast<BS, QUANT>(sbuf, ti, sl2, rvs, m_used, l);
+        const float alpha = fast ? 1.f :
             beta * (masked ? softmax_tile<BS, QUANT, true>(sbuf, ti, sl2, rvs, view, m_used, l)
                            : softmax_tile<BS, QUANT, false>(sbuf, ti, sl2, rvs, view, m_used, l));
-        if (!(flags & kFirst) && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (!fast && !(flags & kFirst) && __any_sync(0xffffffffu, alpha != 1.f)) {
           // O holds the tiles before this one once their last product is done
           ok = wait_all(bar(L::kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
           if (!ok) break;
