@@ -9,7 +9,6 @@
 #include "rotary.cuh"
 #include "step_ops.cuh"
 #include "tree_simt.cuh"
-#include "tree_tc.cuh"
 
 namespace pa {
 namespace {
@@ -40,10 +39,6 @@ int tree_simt_parts(const pa_decode_desc* d, int num_tokens, int max_context_len
   const int64_t rows = std::max<int64_t>(1, (int64_t)num_tokens * d->num_kv_heads);
   const int64_t most = (max_context_len + 511) / 512;
   return (int)std::max<int64_t>(1, std::min<int64_t>(most, (1184 + rows - 1) / rows));
-}
-
-bool tree_tc(const pa_decode_desc* d) {
-  return g_decode_impl.load(std::memory_order_relaxed) != 1 && prefill_tc_supported(d);
 }
 
 size_t tree_simt_bytes(const pa_decode_desc* d, int num_tokens, int max_context_len) {
@@ -252,9 +247,7 @@ size_t paged_attn_tree_workspace_size(const pa_decode_desc* desc, int num_tokens
   if (!tree_desc_ok(desc, num_tokens, max_query_len, max_context_len) || !tree_supported(desc) ||
       desc->num_seqs == 0 || num_tokens == 0 || max_query_len == 0)
     return 0;
-  // either kernel family, so that pa_set_decode_impl does not change it
-  const size_t simt = tree_simt_bytes(desc, num_tokens, max_context_len);
-  return prefill_tc_supported(desc) ? std::max(tree::kWorkspaceBytes, simt) : simt;
+  return tree_simt_bytes(desc, num_tokens, max_context_len);
 }
 
 pa_status paged_attn_tree(const void* q, const void* k_cache, const void* v_cache,
@@ -300,21 +293,17 @@ pa_status paged_attn_tree(const void* q, const void* k_cache, const void* v_cach
   a.q_dtype = desc->q_dtype; a.out_dtype = desc->out_dtype;
   const cudaStream_t st = as_stream(stream);
   cudaError_t e;
-  if (tree_tc(desc)) {
-    e = tree::launch_tc(a, desc->kv_dtype, tree::workspace_at(workspace), st);
-  } else {
-    a.parts = tree_simt_parts(desc, num_tokens, max_context_len);
-    a.part_tokens = (int)round_up((size_t)(max_context_len + a.parts - 1) / a.parts, kSub);
-    const size_t rows = (size_t)num_tokens * desc->num_q_heads * a.parts;
-    a.part_acc = static_cast<float*>(workspace);
-    a.part_m = a.part_acc + rows * desc->head_dim;
-    a.part_l = a.part_m + rows;
-    switch (desc->kv_dtype) {
-      case PA_F32: e = launch_tree_simt_d<PA_F32>(a, desc->head_dim, st); break;
-      case PA_BF16: e = launch_tree_simt_d<PA_BF16>(a, desc->head_dim, st); break;
-      case PA_INT8: e = launch_tree_simt_d<PA_INT8>(a, desc->head_dim, st); break;
-      default: e = launch_tree_simt_d<PA_FP8_E4M3>(a, desc->head_dim, st); break;
-    }
+  a.parts = tree_simt_parts(desc, num_tokens, max_context_len);
+  a.part_tokens = (int)round_up((size_t)(max_context_len + a.parts - 1) / a.parts, kSub);
+  const size_t rows = (size_t)num_tokens * desc->num_q_heads * a.parts;
+  a.part_acc = static_cast<float*>(workspace);
+  a.part_m = a.part_acc + rows * desc->head_dim;
+  a.part_l = a.part_m + rows;
+  switch (desc->kv_dtype) {
+    case PA_F32: e = launch_tree_simt_d<PA_F32>(a, desc->head_dim, st); break;
+    case PA_BF16: e = launch_tree_simt_d<PA_BF16>(a, desc->head_dim, st); break;
+    case PA_INT8: e = launch_tree_simt_d<PA_INT8>(a, desc->head_dim, st); break;
+    default: e = launch_tree_simt_d<PA_FP8_E4M3>(a, desc->head_dim, st); break;
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
