@@ -8,6 +8,7 @@
 
 #include "rotary.cuh"
 #include "step_ops.cuh"
+#include "tree_mma.cuh"
 #include "tree_simt.cuh"
 
 namespace pa {
@@ -41,8 +42,30 @@ int tree_simt_parts(const pa_decode_desc* d, int num_tokens, int max_context_len
   return (int)std::max<int64_t>(1, std::min<int64_t>(most, (1184 + rows - 1) / rows));
 }
 
-size_t tree_simt_bytes(const pa_decode_desc* d, int num_tokens, int max_context_len) {
-  const int parts = tree_simt_parts(d, num_tokens, max_context_len);
+// What the tensor-core kernel takes: bf16 q / out, a bf16, fp8 or int8 cache, head_dim 128, a group
+// that divides its row tiles, blocks of 8, 16 or 32 tokens.
+bool tree_mma(const pa_decode_desc* d) { return prefill_tc_supported(d); }
+
+// Tokens of a part on the tensor cores: about six CTAs for each place on the SMs, so that ragged
+// lengths even out, within 128 (the joining costs more than the split gives below) and kPartMax.
+int tree_mma_part(const pa_decode_desc* d, int max_query_len, int max_context_len) {
+  const int group = d->num_q_heads / d->num_kv_heads, R = tree::mma_rows(max_query_len, group);
+  const int64_t rts = ((int64_t)max_query_len * group + R - 1) / R;
+  const int64_t pairs = rts * d->num_seqs * d->num_kv_heads;
+  const int64_t want = std::max<int64_t>(1, (1776 + pairs - 1) / pairs);
+  const int64_t p = (max_context_len / want + 63) / 64 * 64;
+  return (int)std::min<int64_t>(tree::kPartMax, std::max<int64_t>(128, p));
+}
+
+int parts_of(int max_context_len, int part) {
+  return (int)(((int64_t)max_context_len + part - 1) / part);
+}
+
+size_t tree_bytes(const pa_decode_desc* d, int num_tokens, int max_query_len, int max_context_len) {
+  // either kernel family, so that pa_set_decode_impl does not change it
+  int parts = tree_simt_parts(d, num_tokens, max_context_len);
+  if (tree_mma(d))
+    parts = std::max(parts, parts_of(max_context_len, tree_mma_part(d, max_query_len, max_context_len)));
   return parts == 1 ? 0 : (size_t)num_tokens * d->num_q_heads * parts * (2 + d->head_dim) * 4;
 }
 
@@ -247,7 +270,7 @@ size_t paged_attn_tree_workspace_size(const pa_decode_desc* desc, int num_tokens
   if (!tree_desc_ok(desc, num_tokens, max_query_len, max_context_len) || !tree_supported(desc) ||
       desc->num_seqs == 0 || num_tokens == 0 || max_query_len == 0)
     return 0;
-  return tree_simt_bytes(desc, num_tokens, max_context_len);
+  return tree_bytes(desc, num_tokens, max_query_len, max_context_len);
 }
 
 pa_status paged_attn_tree(const void* q, const void* k_cache, const void* v_cache,
@@ -293,13 +316,24 @@ pa_status paged_attn_tree(const void* q, const void* k_cache, const void* v_cach
   a.q_dtype = desc->q_dtype; a.out_dtype = desc->out_dtype;
   const cudaStream_t st = as_stream(stream);
   cudaError_t e;
-  a.parts = tree_simt_parts(desc, num_tokens, max_context_len);
-  a.part_tokens = (int)round_up((size_t)(max_context_len + a.parts - 1) / a.parts, kSub);
+  const bool mma = tree_mma(desc) && g_decode_impl.load(std::memory_order_relaxed) != 1;
+  if (mma) {
+    a.part_tokens = tree_mma_part(desc, max_query_len, max_context_len);
+    a.parts = parts_of(max_context_len, a.part_tokens);
+  } else {
+    a.parts = tree_simt_parts(desc, num_tokens, max_context_len);
+    a.part_tokens = (int)round_up((size_t)(max_context_len + a.parts - 1) / a.parts, kSub);
+  }
+  a.direct = mma;
   const size_t rows = (size_t)num_tokens * desc->num_q_heads * a.parts;
   a.part_acc = static_cast<float*>(workspace);
   a.part_m = a.part_acc + rows * desc->head_dim;
   a.part_l = a.part_m + rows;
-  switch (desc->kv_dtype) {
+  if (mma) {
+    e = desc->kv_dtype == PA_BF16 ? tree::launch_mma<PA_BF16>(a, st)
+        : desc->kv_dtype == PA_INT8 ? tree::launch_mma<PA_INT8>(a, st)
+                                    : tree::launch_mma<PA_FP8_E4M3>(a, st);
+  } else switch (desc->kv_dtype) {
     case PA_F32: e = launch_tree_simt_d<PA_F32>(a, desc->head_dim, st); break;
     case PA_BF16: e = launch_tree_simt_d<PA_BF16>(a, desc->head_dim, st); break;
     case PA_INT8: e = launch_tree_simt_d<PA_INT8>(a, desc->head_dim, st); break;

@@ -1,0 +1,647 @@
+// Attention of drafted tokens over the paged cache on the tensor cores, with warp-level
+// products (mma.sync m16n8k16).
+//
+// Mathematics: for a tile of R rows, a row being a (drafted token, query head of the kv head's
+// group) pair, S = Q K^T over 64 keys at a time, a running maximum m and sum l per row (log2
+// domain), O = sum 2^(S - m) V; a row sees every key before the drafts and, of the drafts, those
+// in its mask. Parts of one context join as
+//   M = max m_p,  out = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p.
+//
+// Bound: HBM for few rows (a key's K and V cross HBM once for all rows of the tile); the tensor
+// pipe's warp-level rate for 128.
+//
+// Work split: one CTA of four warps per (part of the context, row tile, kv head, sequence). Few
+// rows split a tile's keys over the warps (four warps x 16 keys for 32 rows, two x 32 for 64),
+// which then read and convert every key once, and join at the end; 128 rows give each warp 32.
+// A warp always holds 32 rows: a K or V fragment feeds two products. Keys pass through a ring of
+// shared-memory stages that asynchronous copies fill; zero for what is not there, so that no
+// product reads undefined memory. There are no flags, barriers in memory or waits but the CTA's
+// own.
+//
+// Types: a bf16 cache is multiplied as it is, with P rounded to bf16. Codes of one byte become
+// f16 in registers: E4M3 values and code - zero are exact. Q rows are brought to [2^14, 2^15) by
+// a power of two each, which bf16's eight bits survive down to 2^-28 of the row's largest
+// element. P carries V scale / v_ref * 2^7, v_ref a power of two no smaller than any |V scale| so
+// far: at most 2^15, and f16 holds it to 11 bits down to 2^-21 of the largest.
+#pragma once
+
+#include "decode_tc.cuh"
+#include "tree_simt.cuh"
+
+namespace pa {
+namespace tree {
+
+constexpr int kMmaThreads = 128;
+constexpr int kKeys = 64;             // keys of a tile
+constexpr int kMmaDim = 128;
+constexpr int kPartMax = 4096;        // tokens of a part, at most: their block ids stay in shared memory
+constexpr int kCombRow = kMmaDim + 4; // floats of a row where the warps join
+
+template <pa_dtype KV, int WR>
+struct MmaLayout {
+  static constexpr bool kQuant = KV != PA_BF16;
+  static constexpr int kRowsT = 32 * WR, kWK = 4 / WR;
+  static constexpr int kTileBytes = kKeys * kMmaDim * (kQuant ? 1 : 2);   // K or V of a tile
+  static constexpr int kStages = kQuant ? 4 : WR == 1 ? 3 : 2;
+  static constexpr int kOffQ = kStages * 2 * kTileBytes;
+  static constexpr int kQBytes = kRowsT * 256;
+  static constexpr int kCombBytes = kWK * kRowsT * kCombRow * 4;          // over stages and Q
+  static constexpr int kOffIds = kOffQ + kQBytes > kCombBytes ? kOffQ + kQBytes : kCombBytes;
+  static constexpr int kIds = kPartMax / 8;
+  static constexpr int kOffMl = kOffIds + kIds * 4 * (KV == PA_BF16 ? 1 : KV == PA_INT8 ? 5 : 3);
+  static constexpr int kOffDown = kOffMl + 2 * 128 * 4;
+  static constexpr int kOffOdd = kOffDown + kRowsT * 4;
+  static constexpr int kSmem = kOffOdd + 16 * 4;
+};
+
+// A row's view of a key tile, bit e: the row sees key t0 + e. Keys before `base` are seen, keys
+// at or behind ctx are not.
+__device__ __forceinline__ uint64_t tile_view(const TreeArgs& a, int64_t row, int t0, int base,
+                                              int ctx) {
+  const int below = min(max(base - t0, 0), kKeys);   // keys of the committed context
+  uint64_t v = below >= 64 ? ~0ull : ((1ull << below) - 1ull);
+  if (below < kKeys) {
+    // draft bits from index t0 + below - base on, placed at bit `below`
+    const uint32_t* m = a.tree_mask + row * a.mask_words;
+    const int j0 = t0 + below - base;
+    uint64_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int w = (j0 >> 5) + k;
+      const uint64_t x = w < a.mask_words ? m[w] : 0u;
+      const int sh = 32 * k - (j0 & 31);
+      bits |= sh >= 64 ? 0ull : (sh >= 0 ? x << sh : x >> -sh);
+    }
+    v |= bits << below;
+    const int live = ctx - t0;
+    if (live < kKeys) v &= (1ull << live) - 1ull;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool go) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(go ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+template <int BS, pa_dtype KV, int WR>
+__global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs a) {
+  using L = MmaLayout<KV, WR>;
+  constexpr bool QUANT = L::kQuant;
+  constexpr int R = L::kRowsT, WK = L::kWK, KW = kKeys / WK;   // a warp's keys of a tile
+  constexpr int C = KW < 32 ? KW : 32, NT = C / 8;             // keys of a step, in eights
+  constexpr int MT = 2;
+  constexpr bool HOLD = WR == 1;                               // Q stays in registers
+  constexpr int CPR = QUANT ? 8 : 16;                          // 16-byte chunks of a key
+  extern __shared__ __align__(1024) uint8_t smem[];
+  int* s_id = reinterpret_cast<int*>(smem + L::kOffIds);
+  float* s_ks = reinterpret_cast<float*>(s_id + L::kIds);
+  float* s_vs = s_ks + L::kIds;
+  int* s_kz = reinterpret_cast<int*>(s_vs + L::kIds);
+  int* s_vz = s_kz + L::kIds;
+  float* s_m = reinterpret_cast<float*>(smem + L::kOffMl);     // [WK][R]
+  float* s_l = s_m + 128;
+  float* s_down = reinterpret_cast<float*>(smem + L::kOffDown);
+  uint32_t* s_odd = reinterpret_cast<uint32_t*>(smem + L::kOffOdd);   // [8] drafts, then two flags
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wr = warp % WR, wk = warp / WR, qr = lane >> 2, t = lane & 3;
+  const int Hkv = a.num_kv_heads, G = a.group, TM = R / G;
+  const int part = blockIdx.x, kvh = blockIdx.y % Hkv, rt = blockIdx.y / Hkv, s = blockIdx.z;
+
+  int q0, n, ctx;
+  if (!seq_range(a, s, q0, n, ctx)) {
+    if (part == 0 && blockIdx.y == 0 && tid == 0) flag_error(PA_DEVERR_QUERY);
+    return;
+  }
+  const int t0 = part * a.part_tokens;
+  if (rt * TM >= n || t0 >= ctx) return;
+  const int t1 = min(ctx, t0 + a.part_tokens), base = ctx - n;
+  const int ntiles = (t1 - t0 + kKeys - 1) / kKeys, rows = min(TM, n - rt * TM);
+  const int row0 = q0 + rt * TM;
+
+  if (tid < 10) s_odd[tid] = 0;
+  __syncthreads();
+  // ---- the part's blocks; Q ----
+  {
+    const int32_t* bt = a.block_tables + (int64_t)s * a.max_blocks_per_seq + t0 / BS;
+    const int nb = (t1 - t0 + BS - 1) / BS;
+    // up to the last tile's end; what is not there or cannot be read has id -1 and zeros
+    for (int i = tid; i < ntiles * (kKeys / BS); i += kMmaThreads) {
+      int p = i < nb ? bt[i] : -1;
+      if (i < nb && (p < 0 || p >= a.num_blocks)) {
+        flag_error(PA_DEVERR_BLOCK_ID);
+        p = -1;
+      }
+      if constexpr (QUANT) {
+        const int64_t bh = (int64_t)max(p, 0) * Hkv + kvh;
+        if constexpr (KV == PA_INT8) {
+          const int kz = p >= 0 ? a.k_zeros[bh] : 0, vz = p >= 0 ? a.v_zeros[bh] : 0;
+          if (!zero_in_range(kz) || !zero_in_range(vz)) {
+            flag_error(PA_DEVERR_ZERO);
+            p = -1;
+          }
+          s_kz[i] = p >= 0 ? kz : 0;
+          s_vz[i] = p >= 0 ? vz : 0;
+        }
+        s_ks[i] = p >= 0 ? a.k_scales[bh] : 0.f;
+        s_vs[i] = p >= 0 ? a.v_scales[bh] : 0.f;
+      }
+      s_id[i] = p;
+      if (i < nb && p < 0) s_odd[9] = 1;
+    }
+  }
+  const uint32_t sQ = tc::smem_u32(smem + L::kOffQ);
+  // 16 lanes to a row of 128 channels; a row of no token is zero
+  for (int r = tid >> 4; r < R; r += kMmaThreads / 16) {
+    const int ch = lane & 15;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < rows * G)
+      x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+            ((int64_t)(row0 + r / G) * a.num_q_heads + kvh * G + r % G) * kMmaDim + ch * 8);
+    if constexpr (QUANT) {
+      uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int eb = (int)((__float_as_uint(amax) >> 23) & 0xff);
+      const int e = eb == 0 || eb == 0xff ? 0 : max(-100, min(100, 14 - (eb - 127)));
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
+      x = make_uint4(w[0], w[1], w[2], w[3]);
+      if (ch == 0) s_down[r] = __uint_as_float((uint32_t)(127 - e) << 23);
+    }
+    // chunks XORed so that the fragments below are read without conflicts
+    *reinterpret_cast<uint4*>(smem + L::kOffQ + r * 256 + ((ch ^ (r & (QUANT ? 1 : 7))) << 4)) = x;
+  }
+  __syncthreads();
+  const bool any_bad = s_odd[9] != 0;
+
+  // ---- keys: K and V of tile j into stage j % kStages ----
+  const uint32_t s0 = tc::smem_u32(smem);
+  auto issue = [&](int j) {
+    if (j < ntiles) {
+      const uint32_t dk = s0 + (j % L::kStages) * 2 * L::kTileBytes, dv = dk + L::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < kKeys * CPR / kMmaThreads; ++i) {
+        const int x = tid + i * kMmaThreads, key = x / CPR, c = x % CPR, at = j * kKeys + key;
+        const int p = t0 + at < t1 ? s_id[at / BS] : -1;   // a block's rows behind the context: zero too
+        const int64_t off = (((int64_t)max(p, 0) * Hkv + kvh) * BS + key % BS) * (QUANT ? 128 : 256) + c * 16;
+        const int ck = QUANT ? c ^ (4 * (key & 1)) : c ^ (key & 7), cv = c ^ (key & 7);
+        copy16(dk + key * CPR * 16 + ck * 16, static_cast<const uint8_t*>(a.k_cache) + off, p >= 0);
+        copy16(dv + key * CPR * 16 + cv * 16, static_cast<const uint8_t*>(a.v_cache) + off, p >= 0);
+      }
+    }
+    copies_commit();
+  };
+
+  // A fragments of product step kk (16 channels). Codes: the steps take the channels in the order
+  // in which a lane finds them in a K row: step 4 h + j, lane t: 64 h + 16 t + 4 j .. + 3.
+  uint32_t qh[HOLD ? MT : 1][HOLD ? 8 : 1][4];
+  auto q_bf16 = [&](int mt, int kk, uint32_t (&x)[4]) {
+    const int r = wr * 32 + mt * 16 + (lane & 15), c = kk * 2 + (lane >> 4);
+    tc::ldsm_x4(sQ + r * 256 + ((c ^ (r & 7)) << 4), x);
+  };
+  auto q_f16 = [&](int mt, int h, int b, uint32_t (&x0)[4], uint32_t (&x1)[4]) {  // steps 4h + 2b, + 1
+    const int r = wr * 32 + mt * 16 + qr, c = h * 8 + 2 * t + b;   // r + 8 has r's parity
+    const uint4 u = lds128(sQ + r * 256 + ((c ^ (r & 1)) << 4));
+    const uint4 v = lds128(sQ + (r + 8) * 256 + ((c ^ (r & 1)) << 4));
+    x0[0] = u.x; x0[1] = v.x; x0[2] = u.y; x0[3] = v.y;
+    x1[0] = u.z; x1[1] = v.z; x1[2] = u.w; x1[3] = v.w;
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      if constexpr (QUANT) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q_f16(mt, k >> 1, k & 1, qh[mt][2 * k], qh[mt][2 * k + 1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q_bf16(mt, k, qh[mt][k]);
+      }
+  }
+
+  float o[MT][16][4], m[MT * 2], l[MT * 2], sl2[MT * 2];
+#pragma unroll
+  for (int i = 0; i < MT * 2; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    sl2[i] = a.scale_log2 * (QUANT ? s_down[wr * 32 + i * 8 + qr] : 1.f);
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[mt][i][k] = 0.f;
+  float vref = 0.f;   // codes: the power of two that P's V scales are relative to
+
+#pragma unroll 1
+  for (int j = 0; j < L::kStages - 1; ++j) issue(j);
+#pragma unroll 1
+  for (int j = 0; j < ntiles; ++j) {
+    copies_wait<L::kStages - 2>();
+    __syncthreads();   // tile j is there, and every warp is done with tile j - 1
+    issue(j + L::kStages - 1);
+    const uint32_t sK = s0 + (j % L::kStages) * 2 * L::kTileBytes, sV = sK + L::kTileBytes;
+    const int key0 = t0 + j * kKeys;
+    const bool masked = key0 + kKeys > base || any_bad;
+    uint64_t view[MT * 2];
+    if (masked) {
+      if constexpr (KV != PA_INT8) {
+        // A NaN or infinity in a draft's V row would reach rows that do not see it, as 0 times
+        // itself: it is taken out here and given back at the end to rows that do see it.
+        if (key0 + kKeys > base) {
+          const uint32_t vt = sV - s0;
+          for (int x = tid; x < kKeys * CPR; x += kMmaThreads) {
+            const int key = x / CPR, at = key0 + key;
+            if (at < base || at >= ctx) continue;
+            uint32_t* w = reinterpret_cast<uint32_t*>(smem + vt + key * CPR * 16 + (x % CPR) * 16);
+            bool odd = false;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t keep = ~0u;
+              if constexpr (QUANT) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                  if (((w[i] >> (8 * b)) & 0x7fu) == 0x7fu) keep &= ~(0xffu << (8 * b));
+              } else {
+                if ((w[i] & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+                if ((w[i] & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
+              }
+              if (keep != ~0u) {
+                w[i] &= keep;
+                odd = true;
+              }
+            }
+            if (odd) {
+              atomicOr(&s_odd[(at - base) >> 5], 1u << ((at - base) & 31));
+              s_odd[8] = 1;
+            }
+          }
+          __syncthreads();
+        }
+      }
+      uint64_t gone = 0;
+      if (any_bad) {
+#pragma unroll
+        for (int b = 0; b < kKeys / BS; ++b)
+          if (key0 + b * BS < t1 && s_id[j * (kKeys / BS) + b] < 0) gone |= ((1ull << BS) - 1ull) << (b * BS);
+      }
+#pragma unroll
+      for (int i = 0; i < MT * 2; ++i) {
+        const int tok = min((wr * 32 + i * 8 + qr) / G, rows - 1);
+        view[i] = tile_view(a, row0 + tok, key0, base, ctx) & ~gone;
+      }
+    }
+#pragma unroll 1
+    for (int cc = 0; cc < KW / C; ++cc) {
+      const int k0 = wk * KW + cc * C;     // first of the step's keys in the tile
+      if (key0 + k0 >= t1) break;          // none of them exists (a warp's view: uniform)
+      // ---- S ----
+      float sv[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sv[mt][nt][k] = 0.f;
+      if constexpr (!QUANT) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          uint32_t qa[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            if constexpr (HOLD) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) qa[mt][k] = qh[mt][kk][k];
+            } else {
+              q_bf16(mt, kk, qa[mt]);
+            }
+          }
+#pragma unroll
+          for (int np = 0; np < NT / 2; ++np) {
+            uint32_t b[4];
+            const int key = k0 + np * 16 + (lane & 7) + ((lane >> 4) << 3);
+            const int c = kk * 2 + ((lane >> 3) & 1);
+            tc::ldsm_x4(sK + key * 256 + ((c ^ (key & 7)) << 4), b);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              tc::mma16816<false>(sv[mt][2 * np], qa[mt], b[0], b[1]);
+              tc::mma16816<false>(sv[mt][2 * np + 1], qa[mt], b[2], b[3]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 kc[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int key = k0 + nt * 8 + qr;
+            kc[nt] = lds128(sK + key * 128 + (((t + 4 * h) ^ (4 * (key & 1))) << 4));
+          }
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            uint32_t qa[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              if constexpr (HOLD) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  qa[mt][0][k] = qh[mt][4 * h + 2 * b][k];
+                  qa[mt][1][k] = qh[mt][4 * h + 2 * b + 1][k];
+                }
+              } else {
+                q_f16(mt, h, b, qa[mt][0], qa[mt][1]);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t zc = 0;
+              if constexpr (KV == PA_INT8) {
+                const float z = 1152.f + (float)s_kz[(j * kKeys + k0 + nt * 8) / BS];
+                zc = pack_f16x2(z, z);
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t w = b ? (e ? kc[nt].w : kc[nt].z) : (e ? kc[nt].y : kc[nt].x);
+                uint32_t b0, b1;
+                if constexpr (KV == PA_INT8) {
+                  const uint32_t u = w ^ 0x80808080u;
+                  b0 = tc::i8x2_to_f16x2(u, 0x4140, zc);
+                  b1 = tc::i8x2_to_f16x2(u, 0x4342, zc);
+                } else {
+                  b0 = e4m3x2_to_f16x2((uint16_t)(w & 0xffffu));
+                  b1 = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) tc::mma16816<true>(sv[mt][nt], qa[mt][e], b0, b1);
+              }
+            }
+          }
+        }
+      }
+      // ---- softmax ----
+      float ks[NT], vs[NT], beta = 1.f;
+      if constexpr (QUANT) {
+        float vmax = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int b = (j * kKeys + k0 + nt * 8) / BS;
+          ks[nt] = s_ks[b];
+          vs[nt] = s_vs[b];
+          vmax = fmaxf(vmax, fabsf(vs[nt]));
+        }
+        if (vmax > vref) {
+          // the next power of two, within a range whose reciprocal is one too
+          const int e = max(27, min(227, (int)((__float_as_uint(vmax) >> 23) & 0xff) + 1));
+          const float up = __uint_as_float((uint32_t)e << 23);
+          beta = vref > 0.f ? fminf(vref / up, 1.f) : 1.f;
+          vref = fmaxf(vref, up);
+        }
+        const float rvs = vref > 0.f ? 128.f / vref : 0.f;   // 0: every V scale so far is
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) vs[nt] *= rvs;
+      }
+      float alpha[MT * 2];
+      bool grown = beta != 1.f;
+#pragma unroll
+      for (int i = 0; i < MT * 2; ++i) {
+        const uint32_t v = masked ? (uint32_t)(view[i] >> (k0 + 2 * t)) : ~0u;
+        float mx = m[i];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f = QUANT ? sl2[i] * ks[nt] : sl2[i];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = sv[i >> 1][nt][2 * (i & 1) + e];
+            x *= f;
+            if (masked && !((v >> (nt * 8 + e)) & 1u)) x = -INFINITY;
+            mx = fmaxf(mx, x);
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        alpha[i] = 1.f;
+        if (mx > m[i] + 8.f) {   // lazy: P stays at or below 2^8 otherwise
+          alpha[i] = fast_exp2(m[i] - mx);
+          m[i] = mx;
+          grown = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[mt][i][k] *= alpha[mt * 2 + (k >> 1)] * beta;
+      }
+      uint32_t pf[MT][NT / 2][4];
+#pragma unroll
+      for (int i = 0; i < MT * 2; ++i) {
+        const float ref = m[i] == -INFINITY ? 0.f : m[i];
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p0 = fast_exp2(sv[i >> 1][nt][2 * (i & 1)] - ref);
+          float p1 = fast_exp2(sv[i >> 1][nt][2 * (i & 1) + 1] - ref);
+          sum += p0 + p1;
+          if constexpr (QUANT) {   // P carries its block's V scale; a key that is not seen, none
+            p0 = p0 == 0.f ? 0.f : p0 * vs[nt];
+            p1 = p1 == 0.f ? 0.f : p1 * vs[nt];
+          }
+          pf[i >> 1][nt >> 1][2 * (nt & 1) + (i & 1)] = QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+        }
+        l[i] = l[i] * alpha[i] + sum;
+      }
+      // ---- O += P V ----
+#pragma unroll
+      for (int kp = 0; kp < NT / 2; ++kp) {
+        const int key = k0 + kp * 16 + (lane & 15);
+        uint32_t z0 = 0, z1 = 0;
+        if constexpr (KV == PA_INT8) {
+          const int b = (j * kKeys + k0 + kp * 16) / BS;
+          const float f0 = 1152.f + (float)s_vz[b];
+          const float f1 = 1152.f + (float)s_vz[BS == 8 ? b + 1 : b];
+          z0 = pack_f16x2(f0, f0);
+          z1 = pack_f16x2(f1, f1);
+        }
+        if constexpr (!QUANT) {
+#pragma unroll
+          for (int cb = 0; cb < 8; ++cb) {   // 16 channels
+            uint32_t b[4];
+            tc::ldsm_x4_t(sV + key * 256 + (((cb * 2 + (lane >> 4)) ^ (key & 7)) << 4), b);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              tc::mma16816<false>(o[mt][2 * cb], pf[mt][kp], b[0], b[1]);
+              tc::mma16816<false>(o[mt][2 * cb + 1], pf[mt][kp], b[2], b[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int cb = 0; cb < 4; ++cb) {   // 32 channels
+            uint32_t w[4];   // (keys 0-7, 8-15) x (channels 0-15, 16-31); lane: two keys, two channels
+            tc::ldsm_x4_t(sV + key * 128 + (((cb * 2 + (lane >> 4)) ^ (key & 7)) << 4), w);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t ev[2], od[2];   // the even and the odd channel of both keys
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t u = __byte_perm(w[2 * x + y], 0, 0x3120);
+                if constexpr (KV == PA_INT8) {
+                  const uint32_t ub = u ^ 0x80808080u;
+                  ev[y] = tc::i8x2_to_f16x2(ub, 0x4140, y ? z1 : z0);
+                  od[y] = tc::i8x2_to_f16x2(ub, 0x4342, y ? z1 : z0);
+                } else {
+                  ev[y] = e4m3x2_to_f16x2((uint16_t)(u & 0xffffu));
+                  od[y] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
+                }
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                tc::mma16816<true>(o[mt][4 * cb + 2 * x], pf[mt][kp], ev[0], ev[1]);
+                tc::mma16816<true>(o[mt][4 * cb + 2 * x + 1], pf[mt][kp], od[0], od[1]);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  copies_wait<0>();
+  __syncthreads();   // stages and Q are free: the warps join there
+
+  float* comb = reinterpret_cast<float*>(smem);   // [WK][R][kCombRow]
+  const float unit = QUANT ? vref * (1.f / 128.f) : 1.f;
+#pragma unroll
+  for (int i = 0; i < MT * 2; ++i) {
+    float x = l[i];
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    const int r = wr * 32 + i * 8 + qr;
+    if (t == 0) {
+      s_m[wk * R + r] = m[i];
+      s_l[wk * R + r] = x;
+    }
+    float* d = comb + (wk * R + r) * kCombRow;
+    const int k = 2 * (i & 1);
+#pragma unroll
+    for (int cb = 0; cb < 8; ++cb) {
+      float(&e)[4] = o[i >> 1][2 * cb];
+      float(&f)[4] = o[i >> 1][2 * cb + 1];
+      if constexpr (QUANT) {
+        *reinterpret_cast<float4*>(d + cb * 16 + 4 * t) =
+            make_float4(e[k] * unit, f[k] * unit, e[k + 1] * unit, f[k + 1] * unit);
+      } else {
+        *reinterpret_cast<float2*>(d + cb * 16 + 2 * t) = make_float2(e[k], e[k + 1]);
+        *reinterpret_cast<float2*>(d + cb * 16 + 8 + 2 * t) = make_float2(f[k], f[k + 1]);
+      }
+    }
+  }
+  __syncthreads();
+  const bool whole = ctx <= a.part_tokens, odd = KV != PA_INT8 && s_odd[8] != 0;
+  for (int x = tid; x < rows * G * 32; x += kMmaThreads) {
+    const int r = x >> 5, c = (x & 31) * 4;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) M = fmaxf(M, s_m[w * R + r]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WK; ++w) {
+      const float f = fast_exp2(s_m[w * R + r] - ref);
+      const float4 v = *reinterpret_cast<const float4*>(comb + (w * R + r) * kCombRow + c);
+      sum = fmaf(f, s_l[w * R + r], sum);
+      y.x = fmaf(f, v.x, y.x); y.y = fmaf(f, v.y, y.y); y.z = fmaf(f, v.z, y.z); y.w = fmaf(f, v.w, y.w);
+    }
+    const int64_t trow = row0 + r / G, row = trow * a.num_q_heads + kvh * G + r % G;
+    if (odd) {   // rare
+      float* e = &y.x;
+#pragma unroll 1
+      for (int d = 0; d < n; ++d) {
+        const int key = base + d;
+        if (key < t0 || key >= t1 || !((s_odd[d >> 5] >> (d & 31)) & 1u) ||
+            !((a.tree_mask[trow * a.mask_words + (d >> 5)] >> (d & 31)) & 1u))
+          continue;
+        const int64_t at = (((int64_t)s_id[(key - t0) / BS] * Hkv + kvh) * BS + key % BS) * kMmaDim + c;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (!QUANT) {
+            const float v = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.v_cache)[at + k] << 16);
+            if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) e[k] += v;
+          } else if ((static_cast<const uint8_t*>(a.v_cache)[at + k] & 0x7f) == 0x7f) {
+            e[k] = __uint_as_float(0x7fc00000u);
+          }
+        }
+      }
+    }
+    if (whole) {
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kMmaDim + c) =
+          make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+      if (c == 0 && a.lse_out != nullptr)
+        a.lse_out[row] = sum != 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+    } else {
+      const int64_t pr = row * a.parts + part;
+      *reinterpret_cast<float4*>(a.part_acc + pr * kMmaDim + c) = y;
+      if (c == 0) { a.part_m[pr] = M; a.part_l[pr] = sum; }
+    }
+  }
+}
+
+template <int BS, pa_dtype KV, int WR>
+inline cudaError_t launch_mma_wr(const TreeArgs& a, cudaStream_t st) {
+  using L = MmaLayout<KV, WR>;
+  static_assert(L::kSmem <= 114 * 1024, "two CTAs per SM");
+  static tc::DeviceCache slots;
+  int per_sm = 0;
+  cudaError_t e = tc::resident_per_sm(tree_mma_kernel<BS, KV, WR>, kMmaThreads, L::kSmem, slots, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int tm = L::kRowsT / a.group, rts = (a.max_query_len + tm - 1) / tm;
+  e = launch_pdl(tree_mma_kernel<BS, KV, WR>, dim3(a.parts, rts * a.num_kv_heads, a.num_seqs),
+                 dim3(kMmaThreads), L::kSmem, st, a);
+  if (e != cudaSuccess || a.parts == 1) return e;
+  const int64_t rows = (int64_t)a.num_tokens * a.num_q_heads;
+  return launch_pdl(tree_simt_reduce_kernel<kMmaDim>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a);
+}
+
+// Rows of a tile: as many as the longest draft fills, 32, 64 or 128.
+inline int mma_rows(int max_query_len, int group) {
+  const int most = max_query_len * group;
+  return most <= 32 ? 32 : most <= 64 ? 64 : 128;
+}
+
+template <int BS, pa_dtype KV>
+inline cudaError_t launch_mma_bs(const TreeArgs& a, cudaStream_t st) {
+  switch (mma_rows(a.max_query_len, a.group)) {
+    case 32: return launch_mma_wr<BS, KV, 1>(a, st);
+    case 64: return launch_mma_wr<BS, KV, 2>(a, st);
+    default: return launch_mma_wr<BS, KV, 4>(a, st);
+  }
+}
+
+template <pa_dtype KV>
+inline cudaError_t launch_mma(const TreeArgs& a, cudaStream_t st) {
+  if (a.block_size == 8) return launch_mma_bs<8, KV>(a, st);
+  if (a.block_size == 32) return launch_mma_bs<32, KV>(a, st);
+  return launch_mma_bs<16, KV>(a, st);
+}
+
+}  // namespace tree
+}  // namespace pa

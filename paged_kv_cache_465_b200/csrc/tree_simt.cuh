@@ -1,6 +1,6 @@
 // Attention of drafted tokens over the paged cache on the CUDA cores (fp32 FMA): every
 // supported type, head dimension and group; the path of the shapes that the tensor-core
-// kernel (tree_tc.cuh) does not take, and the reference-precision one.
+// kernel (tree_mma.cuh) does not take, and the reference-precision one.
 //
 // One CTA of 4 warps per (token row, kv head, part of the context), the row's G query heads
 // together. Warps step through 16-key sub-tiles as the decode kernel does, with two
@@ -33,13 +33,13 @@ struct TreeArgs {
   int num_seqs, num_tokens, num_q_heads, num_kv_heads, group;
   int max_blocks_per_seq, num_blocks, block_size, mask_words;
   int max_context_len, max_query_len;
-  int q_rows;                   // tensor-core path: rows of a Q tile in shared memory
   pa_dtype q_dtype, out_dtype;
-  // CUDA-core path: parts of the context
+  // parts of the context
   float* part_m;                // [T][Hq][parts]
   float* part_l;
   float* part_acc;              // [T][Hq][parts][d]
   int part_tokens, parts;
+  int direct;                   // rows of one part are written by the kernel that computes them
 };
 
 // Rows of sequence s: q0 .. q0 + n - 1, the last n of ctx positions. False when the ranges
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) tree_simt_kernel(const TreeAr
   }
 }
 
-// Joins the parts of the CUDA-core path: one warp per (token row, query head), parts in order.
+// Joins the parts: one warp per (token row, query head), parts in order.
 template <int D>
 __global__ void __launch_bounds__(128) tree_simt_reduce_kernel(const TreeArgs a) {
   pdl_wait();
@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(128) tree_simt_reduce_kernel(const TreeArgs a)
   int q0, n, ctx;
   if (!seq_range(a, s, q0, n, ctx) || t < q0 || t >= q0 + n) return;
   const int np = (ctx + a.part_tokens - 1) / a.part_tokens;
+  if (a.direct && np == 1) return;
   const float* pm = a.part_m + row * a.parts;
   const float* pl = a.part_l + row * a.parts;
   float M = -INFINITY;
