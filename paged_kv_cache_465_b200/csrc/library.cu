@@ -46,15 +46,20 @@ int tree_simt_parts(const pa_decode_desc* d, int num_tokens, int max_context_len
 // that divides its row tiles, blocks of 8, 16 or 32 tokens.
 bool tree_mma(const pa_decode_desc* d) { return prefill_tc_supported(d); }
 
-// Tokens of a part on the tensor cores: about six CTAs for each place on the SMs, so that ragged
-// lengths even out, within 128 (the joining costs more than the split gives below) and kPartMax.
+// Tokens of a part on the tensor cores. Few (row tile, sequence, kv head)s: as many parts as make
+// just under 1776 CTAs, two or three rounds for each place on the SMs, when the lengths are alike
+// (8 x 65536 tokens: 27 parts 372 us, 28 parts, which make a round of a few CTAs, 395; 64 parts
+// 456). Many: they fill the places by themselves, and only a context much longer than others is
+// cut, for the last round's sake (256 of 16 .. 8192 tokens: 2048-token parts 246 us, 4096 260; 256
+// of 1024: whole 212 us, halves 283). Parts under 128 tokens cost more to join than they give.
 int tree_mma_part(const pa_decode_desc* d, int max_query_len, int max_context_len) {
   const int group = d->num_q_heads / d->num_kv_heads, R = tree::mma_rows(max_query_len, group);
-  const int64_t rts = ((int64_t)max_query_len * group + R - 1) / R;
-  const int64_t pairs = rts * d->num_seqs * d->num_kv_heads;
-  const int64_t want = std::max<int64_t>(1, (1776 + pairs - 1) / pairs);
-  const int64_t p = (max_context_len / want + 63) / 64 * 64;
-  return (int)std::min<int64_t>(tree::kPartMax, std::max<int64_t>(128, p));
+  const int tm = R / group;
+  const int64_t pairs = (int64_t)((max_query_len + tm - 1) / tm) * d->num_seqs * d->num_kv_heads;
+  constexpr int64_t kCtas = 6 * 296;
+  if (pairs >= kCtas) return 2048;
+  const int64_t want = kCtas / pairs, p = ((int64_t)max_context_len + want - 1) / want;
+  return (int)std::min<int64_t>(tree::kPartMax, std::max<int64_t>(128, (p + 63) / 64 * 64));
 }
 
 int parts_of(int max_context_len, int part) {
@@ -75,9 +80,7 @@ cudaError_t launch_tree_simt(const tree::TreeArgs& a, cudaStream_t st) {
     const dim3 grid(a.num_tokens, a.num_kv_heads, a.parts);
     cudaError_t e = launch_pdl(tree::tree_simt_kernel<KV, D, GP>, grid, dim3(kSimtWarps * 32), 0, st, a);
     if (e != cudaSuccess || a.parts == 1) return e;
-    const int64_t rows = (int64_t)a.num_tokens * a.num_q_heads;
-    return launch_pdl(tree::tree_simt_reduce_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128),
-                      0, st, a);
+    return tree::launch_reduce<D>(a, st);
   } else {
     return cudaErrorInvalidValue;
   }

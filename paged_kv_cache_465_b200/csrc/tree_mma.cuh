@@ -7,16 +7,22 @@
 // in its mask. Parts of one context join as
 //   M = max m_p,  out = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p.
 //
-// Bound: HBM for few rows (a key's K and V cross HBM once for all rows of the tile); the tensor
-// pipe's warp-level rate for 128.
+// Work split: one CTA of four warps per (part of the context, row tile, kv head, sequence). 32 rows
+// split over two pairs of warps (16 rows each), a pair taking half of a tile's keys, and the pairs
+// join at the end; 64 rows are 16 to a warp. 16 rows keep a warp within 168 registers with Q in
+// them, and three CTAs on an SM, which hides each other's waits: against two CTAs of 32 rows to a
+// warp, 256 sequences of 1024 fp8 tokens took 176 us instead of 212 and 8 x 65536 bf16 tokens 352
+// instead of 398. 128 rows do take 32 to a warp, a fragment of K or V then feeding two products
+// (1560 us for 8 x 131072 tokens with 128 rows; two 64-row tiles, the second reading K and V from
+// L2, 1741).
+// Keys pass through a ring of shared-memory stages that asynchronous copies fill; zero for what is
+// not there, so that no product reads undefined memory. There are no flags or barriers in memory
+// and no waits but the CTA's own.
 //
-// Work split: one CTA of four warps per (part of the context, row tile, kv head, sequence). Few
-// rows split a tile's keys over the warps (four warps x 16 keys for 32 rows, two x 32 for 64),
-// which then read and convert every key once, and join at the end; 128 rows give each warp 32.
-// A warp always holds 32 rows: a K or V fragment feeds two products. Keys pass through a ring of
-// shared-memory stages that asynchronous copies fill; zero for what is not there, so that no
-// product reads undefined memory. There are no flags, barriers in memory or waits but the CTA's
-// own.
+// Bound: HBM for a bf16 cache and up to 32 rows (8 x 65536 tokens: 352 us, 93 % of the measured
+// copy rate). Beyond, and for codes, the latency of the chain fragment - product - softmax - product
+// in the few warps that registers leave: the tensor pipe is busy 33 - 38 % of the time, the issue
+// slots 30 - 40 %, and HBM gets to 47 % (8 x 65536 fp8 tokens 312 us).
 //
 // Types: a bf16 cache is multiplied as it is, with P rounded to bf16. Codes of one byte become
 // f16 in registers: E4M3 values and code - zero are exact. Q rows are brought to [2^14, 2^15) by
@@ -34,17 +40,21 @@ namespace tree {
 constexpr int kMmaThreads = 128;
 constexpr int kKeys = 64;             // keys of a tile
 constexpr int kMmaDim = 128;
-constexpr int kPartMax = 4096;        // tokens of a part, at most: their block ids stay in shared memory
+constexpr int kPartMax = 5120;        // tokens of a part, at most: their block ids stay in shared memory
 constexpr int kCombRow = kMmaDim + 4; // floats of a row where the warps join
 
-template <pa_dtype KV, int WR>
+template <pa_dtype KV, int MT, int WR>
 struct MmaLayout {
   static constexpr bool kQuant = KV != PA_BF16;
-  static constexpr int kRowsT = 32 * WR, kWK = 4 / WR;
+  static constexpr int kRowsT = 16 * MT * WR, kWK = 4 / WR;
   static constexpr int kTileBytes = kKeys * kMmaDim * (kQuant ? 1 : 2);   // K or V of a tile
-  static constexpr int kStages = kQuant ? 4 : WR == 1 ? 3 : 2;
-  static constexpr int kOffQ = kStages * 2 * kTileBytes;
-  static constexpr int kQBytes = kRowsT * 256;
+  static constexpr int kStages = kQuant ? (MT == 1 ? 3 : 4) : 2;
+  static constexpr int kCtas = MT == 1 ? 3 : 2;                           // on an SM
+  static constexpr bool kHold = MT == 1;                                  // Q stays in registers
+  // Q that goes to registers waits in the last stage, which is filled after that
+  static constexpr int kOffQ = (kHold ? kStages - 1 : kStages) * 2 * kTileBytes;
+  static constexpr int kQBytes = kHold ? 2 * kTileBytes : kRowsT * 256;
+  static_assert(!kHold || kRowsT * 256 <= 2 * kTileBytes, "Q fits a stage");
   static constexpr int kCombBytes = kWK * kRowsT * kCombRow * 4;          // over stages and Q
   static constexpr int kOffIds = kOffQ + kQBytes > kCombBytes ? kOffQ + kQBytes : kCombBytes;
   static constexpr int kIds = kPartMax / 8;
@@ -93,14 +103,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   return v;
 }
 
-template <int BS, pa_dtype KV, int WR>
-__global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs a) {
-  using L = MmaLayout<KV, WR>;
+template <int BS, pa_dtype KV, int MT, int WR>
+__global__ void __launch_bounds__(kMmaThreads, MmaLayout<KV, MT, WR>::kCtas) tree_mma_kernel(const TreeArgs a, int rts) {
+  using L = MmaLayout<KV, MT, WR>;
   constexpr bool QUANT = L::kQuant;
   constexpr int R = L::kRowsT, WK = L::kWK, KW = kKeys / WK;   // a warp's keys of a tile
   constexpr int C = KW < 32 ? KW : 32, NT = C / 8;             // keys of a step, in eights
-  constexpr int MT = 2;
-  constexpr bool HOLD = WR == 1;                               // Q stays in registers
+  constexpr bool HOLD = L::kHold;                              // Q stays in registers
   constexpr int CPR = QUANT ? 8 : 16;                          // 16-byte chunks of a key
   extern __shared__ __align__(1024) uint8_t smem[];
   int* s_id = reinterpret_cast<int*>(smem + L::kOffIds);
@@ -117,11 +126,12 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wr = warp % WR, wk = warp / WR, qr = lane >> 2, t = lane & 3;
   const int Hkv = a.num_kv_heads, G = a.group, TM = R / G;
-  const int part = blockIdx.x, kvh = blockIdx.y % Hkv, rt = blockIdx.y / Hkv, s = blockIdx.z;
+  // row tiles of the same keys are neighbours: the second finds them in L2
+  const int part = blockIdx.x / rts, rt = blockIdx.x % rts, kvh = blockIdx.y, s = blockIdx.z;
 
   int q0, n, ctx;
   if (!seq_range(a, s, q0, n, ctx)) {
-    if (part == 0 && blockIdx.y == 0 && tid == 0) flag_error(PA_DEVERR_QUERY);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) flag_error(PA_DEVERR_QUERY);
     return;
   }
   const int t0 = part * a.part_tokens;
@@ -132,7 +142,19 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
 
   if (tid < 10) s_odd[tid] = 0;
   __syncthreads();
-  // ---- the part's blocks; Q ----
+  // ---- Q on its way; the part's blocks ----
+  // 16 lanes to a row of 128 channels; a row of no token is zero
+  constexpr int kQIts = R / (kMmaThreads / 16);
+  const int ch = lane & 15;
+  uint4 qx[kQIts];
+#pragma unroll
+  for (int i = 0; i < kQIts; ++i) {
+    const int r = (tid >> 4) + i * (kMmaThreads / 16);
+    qx[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows * G)
+      qx[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                ((int64_t)(row0 + r / G) * a.num_q_heads + kvh * G + r % G) * kMmaDim + ch * 8);
+  }
   {
     const int32_t* bt = a.block_tables + (int64_t)s * a.max_blocks_per_seq + t0 / BS;
     const int nb = (t1 - t0 + BS - 1) / BS;
@@ -161,14 +183,41 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
       if (i < nb && p < 0) s_odd[9] = 1;
     }
   }
+  __syncthreads();
+  const bool any_bad = s_odd[9] != 0;
+
+  // ---- keys: K and V of tile j into stage j % kStages ----
+  const uint32_t s0 = tc::smem_u32(smem);
+  const int64_t bstride = (int64_t)Hkv * BS * (CPR * 16);
+  const int c0 = tid % CPR, key00 = tid / CPR;   // a thread's copies are of one chunk, kKeyStep keys apart
+  constexpr int kKeyStep = kMmaThreads / CPR;
+  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_cache) + (int64_t)kvh * BS * (CPR * 16) + c0 * 16;
+  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache) + (int64_t)kvh * BS * (CPR * 16) + c0 * 16;
+  auto issue = [&](int j) {
+    if (j < ntiles) {
+      const uint32_t dk = s0 + (j % L::kStages) * 2 * L::kTileBytes, dv = dk + L::kTileBytes;
+      const int live = t1 - t0 - j * kKeys;
+      const int* ids = s_id + j * (kKeys / BS);
+#pragma unroll
+      for (int i = 0; i < kKeys / kKeyStep; ++i) {
+        const int key = key00 + i * kKeyStep;
+        const int p = key < live ? ids[key / BS] : -1;   // a block's rows behind the context: zero too
+        const int64_t off = (int64_t)max(p, 0) * bstride + (key % BS) * (CPR * 16);
+        const int ck = QUANT ? c0 ^ (4 * (key & 1)) : c0 ^ (key & 7), cv = c0 ^ (key & 7);
+        copy16(dk + key * CPR * 16 + ck * 16, kbase + off, p >= 0);
+        copy16(dv + key * CPR * 16 + cv * 16, vbase + off, p >= 0);
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll 1
+  for (int j = 0; j < L::kStages - 1; ++j) issue(j);
+
   const uint32_t sQ = tc::smem_u32(smem + L::kOffQ);
-  // 16 lanes to a row of 128 channels; a row of no token is zero
-  for (int r = tid >> 4; r < R; r += kMmaThreads / 16) {
-    const int ch = lane & 15;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < rows * G)
-      x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-            ((int64_t)(row0 + r / G) * a.num_q_heads + kvh * G + r % G) * kMmaDim + ch * 8);
+#pragma unroll
+  for (int i = 0; i < kQIts; ++i) {
+    const int r = (tid >> 4) + i * (kMmaThreads / 16);
+    uint4 x = qx[i];
     if constexpr (QUANT) {
       uint32_t w[4] = {x.x, x.y, x.z, x.w};
       float amax = 0.f;
@@ -188,35 +237,16 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
     *reinterpret_cast<uint4*>(smem + L::kOffQ + r * 256 + ((ch ^ (r & (QUANT ? 1 : 7))) << 4)) = x;
   }
   __syncthreads();
-  const bool any_bad = s_odd[9] != 0;
-
-  // ---- keys: K and V of tile j into stage j % kStages ----
-  const uint32_t s0 = tc::smem_u32(smem);
-  auto issue = [&](int j) {
-    if (j < ntiles) {
-      const uint32_t dk = s0 + (j % L::kStages) * 2 * L::kTileBytes, dv = dk + L::kTileBytes;
-#pragma unroll
-      for (int i = 0; i < kKeys * CPR / kMmaThreads; ++i) {
-        const int x = tid + i * kMmaThreads, key = x / CPR, c = x % CPR, at = j * kKeys + key;
-        const int p = t0 + at < t1 ? s_id[at / BS] : -1;   // a block's rows behind the context: zero too
-        const int64_t off = (((int64_t)max(p, 0) * Hkv + kvh) * BS + key % BS) * (QUANT ? 128 : 256) + c * 16;
-        const int ck = QUANT ? c ^ (4 * (key & 1)) : c ^ (key & 7), cv = c ^ (key & 7);
-        copy16(dk + key * CPR * 16 + ck * 16, static_cast<const uint8_t*>(a.k_cache) + off, p >= 0);
-        copy16(dv + key * CPR * 16 + cv * 16, static_cast<const uint8_t*>(a.v_cache) + off, p >= 0);
-      }
-    }
-    copies_commit();
-  };
 
   // A fragments of product step kk (16 channels). Codes: the steps take the channels in the order
   // in which a lane finds them in a K row: step 4 h + j, lane t: 64 h + 16 t + 4 j .. + 3.
   uint32_t qh[HOLD ? MT : 1][HOLD ? 8 : 1][4];
   auto q_bf16 = [&](int mt, int kk, uint32_t (&x)[4]) {
-    const int r = wr * 32 + mt * 16 + (lane & 15), c = kk * 2 + (lane >> 4);
+    const int r = wr * 16 * MT + mt * 16 + (lane & 15), c = kk * 2 + (lane >> 4);
     tc::ldsm_x4(sQ + r * 256 + ((c ^ (r & 7)) << 4), x);
   };
   auto q_f16 = [&](int mt, int h, int b, uint32_t (&x0)[4], uint32_t (&x1)[4]) {  // steps 4h + 2b, + 1
-    const int r = wr * 32 + mt * 16 + qr, c = h * 8 + 2 * t + b;   // r + 8 has r's parity
+    const int r = wr * 16 * MT + mt * 16 + qr, c = h * 8 + 2 * t + b;   // r + 8 has r's parity
     const uint4 u = lds128(sQ + r * 256 + ((c ^ (r & 1)) << 4));
     const uint4 v = lds128(sQ + (r + 8) * 256 + ((c ^ (r & 1)) << 4));
     x0[0] = u.x; x0[1] = v.x; x0[2] = u.y; x0[3] = v.y;
@@ -239,7 +269,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
   for (int i = 0; i < MT * 2; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-    sl2[i] = a.scale_log2 * (QUANT ? s_down[wr * 32 + i * 8 + qr] : 1.f);
+    sl2[i] = a.scale_log2 * (QUANT ? s_down[wr * 16 * MT + i * 8 + qr] : 1.f);
   }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -249,8 +279,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
       for (int k = 0; k < 4; ++k) o[mt][i][k] = 0.f;
   float vref = 0.f;   // codes: the power of two that P's V scales are relative to
 
-#pragma unroll 1
-  for (int j = 0; j < L::kStages - 1; ++j) issue(j);
 #pragma unroll 1
   for (int j = 0; j < ntiles; ++j) {
     copies_wait<L::kStages - 2>();
@@ -303,7 +331,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
       }
 #pragma unroll
       for (int i = 0; i < MT * 2; ++i) {
-        const int tok = min((wr * 32 + i * 8 + qr) / G, rows - 1);
+        const int tok = min((wr * 16 * MT + i * 8 + qr) / G, rows - 1);
         view[i] = tile_view(a, row0 + tok, key0, base, ctx) & ~gone;
       }
     }
@@ -417,6 +445,42 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) vs[nt] *= rvs;
       }
+      uint32_t pf[MT][NT / 2][4];
+      // P against the standing reference, without looking for the maximum: right when no lane's
+      // sum passes 2^8 (a score that outgrew the reference, or is no number, makes one)
+      auto weights = [&](int i, float f0, bool scaled) {
+        const float ref = m[i] == -INFINITY && scaled ? 0.f : -m[i];
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f = scaled ? 1.f : QUANT ? f0 * ks[nt] : f0;
+          float p0 = fast_exp2(fmaf(sv[i >> 1][nt][2 * (i & 1)], f, ref));
+          float p1 = fast_exp2(fmaf(sv[i >> 1][nt][2 * (i & 1) + 1], f, ref));
+          sum += p0 + p1;
+          if constexpr (QUANT) {   // P carries its block's V scale; a key that is not seen, none
+            p0 = scaled && p0 == 0.f ? 0.f : p0 * vs[nt];
+            p1 = scaled && p1 == 0.f ? 0.f : p1 * vs[nt];
+          }
+          pf[i >> 1][nt >> 1][2 * (nt & 1) + (i & 1)] = QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+        }
+        return sum;
+      };
+      bool fast = false;
+      if (!masked && beta == 1.f) {
+        float sum[MT * 2];
+        bool good = true;
+#pragma unroll
+        for (int i = 0; i < MT * 2; ++i) {
+          sum[i] = weights(i, sl2[i], false);
+          good = good && sum[i] <= 256.f;
+        }
+        fast = __all_sync(0xffffffffu, good);
+        if (fast) {
+#pragma unroll
+          for (int i = 0; i < MT * 2; ++i) l[i] += sum[i];
+        }
+      }
+      if (!fast) {
       float alpha[MT * 2];
       bool grown = beta != 1.f;
 #pragma unroll
@@ -451,23 +515,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[mt][i][k] *= alpha[mt * 2 + (k >> 1)] * beta;
       }
-      uint32_t pf[MT][NT / 2][4];
 #pragma unroll
-      for (int i = 0; i < MT * 2; ++i) {
-        const float ref = m[i] == -INFINITY ? 0.f : m[i];
-        float sum = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p0 = fast_exp2(sv[i >> 1][nt][2 * (i & 1)] - ref);
-          float p1 = fast_exp2(sv[i >> 1][nt][2 * (i & 1) + 1] - ref);
-          sum += p0 + p1;
-          if constexpr (QUANT) {   // P carries its block's V scale; a key that is not seen, none
-            p0 = p0 == 0.f ? 0.f : p0 * vs[nt];
-            p1 = p1 == 0.f ? 0.f : p1 * vs[nt];
-          }
-          pf[i >> 1][nt >> 1][2 * (nt & 1) + (i & 1)] = QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-        }
-        l[i] = l[i] * alpha[i] + sum;
+      for (int i = 0; i < MT * 2; ++i) l[i] = l[i] * alpha[i] + weights(i, 1.f, true);
       }
       // ---- O += P V ----
 #pragma unroll
@@ -533,7 +582,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
     float x = l[i];
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     x += __shfl_xor_sync(0xffffffffu, x, 2);
-    const int r = wr * 32 + i * 8 + qr;
+    const int r = wr * 16 * MT + i * 8 + qr;
     if (t == 0) {
       s_m[wk * R + r] = m[i];
       s_l[wk * R + r] = x;
@@ -605,20 +654,19 @@ __global__ void __launch_bounds__(kMmaThreads, 2) tree_mma_kernel(const TreeArgs
   }
 }
 
-template <int BS, pa_dtype KV, int WR>
+template <int BS, pa_dtype KV, int MT, int WR>
 inline cudaError_t launch_mma_wr(const TreeArgs& a, cudaStream_t st) {
-  using L = MmaLayout<KV, WR>;
-  static_assert(L::kSmem <= 114 * 1024, "two CTAs per SM");
+  using L = MmaLayout<KV, MT, WR>;
+  static_assert(L::kCtas * (L::kSmem + 1024) <= 228 * 1024, "CTAs on an SM");
   static tc::DeviceCache slots;
   int per_sm = 0;
-  cudaError_t e = tc::resident_per_sm(tree_mma_kernel<BS, KV, WR>, kMmaThreads, L::kSmem, slots, &per_sm);
+  cudaError_t e = tc::resident_per_sm(tree_mma_kernel<BS, KV, MT, WR>, kMmaThreads, L::kSmem, slots, &per_sm);
   if (e != cudaSuccess) return e;
   const int tm = L::kRowsT / a.group, rts = (a.max_query_len + tm - 1) / tm;
-  e = launch_pdl(tree_mma_kernel<BS, KV, WR>, dim3(a.parts, rts * a.num_kv_heads, a.num_seqs),
-                 dim3(kMmaThreads), L::kSmem, st, a);
+  e = launch_pdl(tree_mma_kernel<BS, KV, MT, WR>, dim3(a.parts * rts, a.num_kv_heads, a.num_seqs),
+                 dim3(kMmaThreads), L::kSmem, st, a, rts);
   if (e != cudaSuccess || a.parts == 1) return e;
-  const int64_t rows = (int64_t)a.num_tokens * a.num_q_heads;
-  return launch_pdl(tree_simt_reduce_kernel<kMmaDim>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a);
+  return launch_reduce<kMmaDim>(a, st);
 }
 
 // Rows of a tile: as many as the longest draft fills, 32, 64 or 128.
@@ -630,9 +678,9 @@ inline int mma_rows(int max_query_len, int group) {
 template <int BS, pa_dtype KV>
 inline cudaError_t launch_mma_bs(const TreeArgs& a, cudaStream_t st) {
   switch (mma_rows(a.max_query_len, a.group)) {
-    case 32: return launch_mma_wr<BS, KV, 1>(a, st);
-    case 64: return launch_mma_wr<BS, KV, 2>(a, st);
-    default: return launch_mma_wr<BS, KV, 4>(a, st);
+    case 32: return launch_mma_wr<BS, KV, 1, 2>(a, st);
+    case 64: return launch_mma_wr<BS, KV, 1, 4>(a, st);
+    default: return launch_mma_wr<BS, KV, 2, 4>(a, st);
   }
 }
 

@@ -39,6 +39,7 @@ struct TreeArgs {
   float* part_l;
   float* part_acc;              // [T][Hq][parts][d]
   int part_tokens, parts;
+  int reduce_heads;             // of a warp of the joining kernel
   int direct;                   // rows of one part are written by the kernel that computes them
 };
 
@@ -247,42 +248,58 @@ __global__ void __launch_bounds__(kSimtWarps * 32) tree_simt_kernel(const TreeAr
   }
 }
 
-// Joins the parts: one warp per (token row, query head), parts in order.
+// Joins the parts, in order: one warp per (token row, a.reduce_heads query heads). Bound by latency:
+// rows of one part leave as soon as their sequence is known.
+
 template <int D>
-__global__ void __launch_bounds__(128) tree_simt_reduce_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(128) tree_reduce_kernel(const TreeArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (int64_t)a.num_tokens * a.num_q_heads) return;
-  const int t = (int)(row / a.num_q_heads);
+  const int lane = threadIdx.x & 31, groups = (a.num_q_heads + a.reduce_heads - 1) / a.reduce_heads;
+  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (w >= (int64_t)a.num_tokens * groups) return;
+  const int t = (int)(w / groups), h0 = (int)(w % groups) * a.reduce_heads;
   const int s = seq_of_row(a.query_start, a.num_seqs, t);
   int q0, n, ctx;
   if (!seq_range(a, s, q0, n, ctx) || t < q0 || t >= q0 + n) return;
   const int np = (ctx + a.part_tokens - 1) / a.part_tokens;
   if (a.direct && np == 1) return;
-  const float* pm = a.part_m + row * a.parts;
-  const float* pl = a.part_l + row * a.parts;
-  float M = -INFINITY;
-  for (int p = lane; p < np; p += 32) M = fmaxf(M, pm[p]);
+#pragma unroll 1
+  for (int h = h0; h < min(a.num_q_heads, h0 + a.reduce_heads); ++h) {
+    const int64_t row = (int64_t)t * a.num_q_heads + h;
+    const float* pm = a.part_m + row * a.parts;
+    const float* pl = a.part_l + row * a.parts;
+    float M = -INFINITY;
+    for (int p = lane; p < np; p += 32) M = fmaxf(M, pm[p]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float acc[D / 32], L = 0.f;
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float acc[D / 32], L = 0.f;
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
-  for (int p = 0; p < np; ++p) {
-    const float w = fast_exp2(pm[p] - ref);
-    L = fmaf(w, pl[p], L);
-    const float* src = a.part_acc + (row * a.parts + p) * D;
+    for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < np; ++p) {
+      const float f = fast_exp2(pm[p] - ref);
+      L = fmaf(f, pl[p], L);
+      const float* src = a.part_acc + (row * a.parts + p) * D;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(w, src[lane + 32 * j], acc[j]);
+      for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(f, src[lane + 32 * j], acc[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      store_out(a.out, a.out_dtype, row * D + lane + 32 * j, L != 0.f ? acc[j] / L : 0.f);
+    if (lane == 0 && a.lse_out != nullptr)
+      a.lse_out[row] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
   }
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j)
-    store_out(a.out, a.out_dtype, row * D + lane + 32 * j, L != 0.f ? acc[j] / L : 0.f);
-  if (lane == 0 && a.lse_out != nullptr)
-    a.lse_out[row] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+inline cudaError_t launch_reduce(TreeArgs a, cudaStream_t st) {
+  // Four heads to a warp where there are rows enough to fill the SMs several times over (256
+  // sequences, most of one part: 16400 CTAs of one head to a warp took 19 us).
+  a.reduce_heads = (int64_t)a.num_tokens * a.num_q_heads >= 32768 ? 4 : 1;
+  const int64_t warps = (int64_t)a.num_tokens * ((a.num_q_heads + a.reduce_heads - 1) / a.reduce_heads);
+  return launch_pdl(tree_reduce_kernel<D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, a);
 }
 
 }  // namespace tree
