@@ -14,6 +14,8 @@ paged      Slot mapping, the reference block allocator (free queue, ref_count, f
            append with copy-on-write), the slot-mapped cache write and the block copy.
 attention  Decode attention: gather each sequence's K/V through its block table into
            contiguous arrays, then softmax(q K^T * scale) V in float64.
+drafted    A drafted step: tables, slots, positions and masks from request lengths, rotary
+           turn and cache write, tree attention, acceptance and the move of accepted rows.
 
 Sources are cited as page title + section of the four pages on KV caches and PagedAttention:
   [KVFail]   "Transformer inference KV-cache memory-management failure modes"
