@@ -93,9 +93,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool go) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(go ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -104,7 +108,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
 }
 
 template <int BS, pa_dtype KV, int MT, int WR>
-__global__ void __launch_bounds__(kMmaThreads, MmaLayout<KV, MT, WR>::kCtas) tree_mma_kernel(const TreeArgs a, int rts) {
+__global__ void __launch_bounds__(kMmaThreads, MmaLayout<KV, MT, WR>::kCtas)
+tree_mma_kernel(const TreeArgs a, int rts) {
   using L = MmaLayout<KV, MT, WR>;
   constexpr bool QUANT = L::kQuant;
   constexpr int R = L::kRowsT, WK = L::kWK, KW = kKeys / WK;   // a warp's keys of a tile
@@ -189,10 +194,12 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KV, MT, WR>::kCtas) tre
   // ---- keys: K and V of tile j into stage j % kStages ----
   const uint32_t s0 = tc::smem_u32(smem);
   const int64_t bstride = (int64_t)Hkv * BS * (CPR * 16);
-  const int c0 = tid % CPR, key00 = tid / CPR;   // a thread's copies are of one chunk, kKeyStep keys apart
+  // a thread's copies are of one chunk, kKeyStep keys apart
+  const int c0 = tid % CPR, key00 = tid / CPR;
   constexpr int kKeyStep = kMmaThreads / CPR;
-  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_cache) + (int64_t)kvh * BS * (CPR * 16) + c0 * 16;
-  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache) + (int64_t)kvh * BS * (CPR * 16) + c0 * 16;
+  const int64_t head_off = (int64_t)kvh * BS * (CPR * 16) + c0 * 16;
+  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_cache) + head_off;
+  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache) + head_off;
   auto issue = [&](int j) {
     if (j < ntiles) {
       const uint32_t dk = s0 + (j % L::kStages) * 2 * L::kTileBytes, dv = dk + L::kTileBytes;
@@ -201,7 +208,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KV, MT, WR>::kCtas) tre
 #pragma unroll
       for (int i = 0; i < kKeys / kKeyStep; ++i) {
         const int key = key00 + i * kKeyStep;
-        const int p = key < live ? ids[key / BS] : -1;   // a block's rows behind the context: zero too
+        // a block's rows behind the context are zero too
+        const int p = key < live ? ids[key / BS] : -1;
         const int64_t off = (int64_t)max(p, 0) * bstride + (key % BS) * (CPR * 16);
         const int ck = QUANT ? c0 ^ (4 * (key & 1)) : c0 ^ (key & 7), cv = c0 ^ (key & 7);
         copy16(dk + key * CPR * 16 + ck * 16, kbase + off, p >= 0);
@@ -222,14 +230,15 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KV, MT, WR>::kCtas) tre
       uint32_t w[4] = {x.x, x.y, x.z, x.w};
       float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+      for (int k = 0; k < 4; ++k)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const int eb = (int)((__float_as_uint(amax) >> 23) & 0xff);
       const int e = eb == 0 || eb == 0xff ? 0 : max(-100, min(100, 14 - (eb - 127)));
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
+      for (int k = 0; k < 4; ++k) w[k] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
       x = make_uint4(w[0], w[1], w[2], w[3]);
       if (ch == 0) s_down[r] = __uint_as_float((uint32_t)(127 - e) << 23);
     }
@@ -481,42 +490,42 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KV, MT, WR>::kCtas) tre
         }
       }
       if (!fast) {
-      float alpha[MT * 2];
-      bool grown = beta != 1.f;
+        float alpha[MT * 2];
+        bool grown = beta != 1.f;
 #pragma unroll
-      for (int i = 0; i < MT * 2; ++i) {
-        const uint32_t v = masked ? (uint32_t)(view[i] >> (k0 + 2 * t)) : ~0u;
-        float mx = m[i];
+        for (int i = 0; i < MT * 2; ++i) {
+          const uint32_t v = masked ? (uint32_t)(view[i] >> (k0 + 2 * t)) : ~0u;
+          float mx = m[i];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float f = QUANT ? sl2[i] * ks[nt] : sl2[i];
+          for (int nt = 0; nt < NT; ++nt) {
+            const float f = QUANT ? sl2[i] * ks[nt] : sl2[i];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& x = sv[i >> 1][nt][2 * (i & 1) + e];
-            x *= f;
-            if (masked && !((v >> (nt * 8 + e)) & 1u)) x = -INFINITY;
-            mx = fmaxf(mx, x);
+            for (int e = 0; e < 2; ++e) {
+              float& x = sv[i >> 1][nt][2 * (i & 1) + e];
+              x *= f;
+              if (masked && !((v >> (nt * 8 + e)) & 1u)) x = -INFINITY;
+              mx = fmaxf(mx, x);
+            }
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          alpha[i] = 1.f;
+          if (mx > m[i] + 8.f) {   // lazy: P stays at or below 2^8 otherwise
+            alpha[i] = fast_exp2(m[i] - mx);
+            m[i] = mx;
+            grown = true;
           }
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        alpha[i] = 1.f;
-        if (mx > m[i] + 8.f) {   // lazy: P stays at or below 2^8 otherwise
-          alpha[i] = fast_exp2(m[i] - mx);
-          m[i] = mx;
-          grown = true;
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[mt][i][k] *= alpha[mt * 2 + (k >> 1)] * beta;
         }
-      }
-      if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[mt][i][k] *= alpha[mt * 2 + (k >> 1)] * beta;
-      }
-#pragma unroll
-      for (int i = 0; i < MT * 2; ++i) l[i] = l[i] * alpha[i] + weights(i, 1.f, true);
+        for (int i = 0; i < MT * 2; ++i) l[i] = l[i] * alpha[i] + weights(i, 1.f, true);
       }
       // ---- O += P V ----
 #pragma unroll

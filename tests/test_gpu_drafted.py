@@ -654,6 +654,40 @@ def test_tree_results_repeat_and_do_not_depend_on_placement(pa, impl, kv):
     assert torch.equal(o1, o2) and torch.equal(l1, l2)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("new", [40, 5])
+def test_tree_drafts_across_the_parts_of_a_context(pa, kv, new):
+    """A small batch is cut every 128 tokens: drafts that end, begin and lie across a cut, and a
+    part that holds nothing but drafts."""
+    Tree(21, [100, 88, 127, 128, 250, 384, 0], [new] * 7, 4, 1, 128, 8, kv).check(pa)
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_tree_lengths_far_below_the_longest_allowed(pa, impl, kv):
+    """A table and a longest context made for more than the batch has: most parts are empty, and
+    rows of one part meet rows of several."""
+    t = Tree(22, [30, 700, 3, 260], [4, 9, 1, 2], 8, 2, 128, 16, kv)
+    t.bt = np.concatenate([t.bt, np.full((4, 900), -1)], 1)
+    t.max_ctx = 16 * 900
+    t.device()
+    t.check(pa, impl)
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("kv", ["fp8", "int8"])
+def test_tree_scales_of_either_sign_that_differ_between_blocks(pa, impl, kv):
+    """Block scales times powers of two from 2^-6 to 2^6 with signs, growing and shrinking along a
+    context: weights that carry them stay within the format they are rounded to."""
+    t = Tree(23, [330, 40, 500], [6, 8, 3], 8, 2, 128, 16, kv)
+    rng = np.random.default_rng(24)
+    for n, e in (("k_scales", 2), ("v_scales", 6)):
+        shape = t.o[n].shape
+        t.o[n] *= (rng.choice([-1.0, 1.0], shape) * 2.0 ** rng.integers(-e, e + 1, shape)).astype(np.float32)
+    t.device()
+    t.check(pa, impl)
+
+
 def test_tree_two_calls_at_once_and_other_streams(pa):
     """Calls on two streams with a workspace each, and on a side stream, give the same results."""
     a, b = Tree(16, [3000, 40], [8, 5], 8, 2, 128, 16, "bf16"), Tree(17, [700] * 9, [4] * 9, 8, 2, 128, 16, "fp8")
