@@ -52,14 +52,20 @@ bool tree_mma(const pa_decode_desc* d) { return prefill_tc_supported(d); }
 // 456). Many: they fill the places by themselves, and only a context much longer than others is
 // cut, for the last round's sake (256 of 16 .. 8192 tokens: 2048-token parts 246 us, 4096 260; 256
 // of 1024: whole 212 us, halves 283). Parts under 128 tokens cost more to join than they give.
-int tree_mma_part(const pa_decode_desc* d, int max_query_len, int max_context_len) {
+// The parts' results stay within 192 MB (a thousandth of the GPU's memory): longer parts otherwise.
+int tree_mma_part(const pa_decode_desc* d, int num_tokens, int max_query_len,
+                  int max_context_len) {
   const int group = d->num_q_heads / d->num_kv_heads, R = tree::mma_rows(max_query_len, group);
   const int tm = R / group;
   const int64_t pairs = (int64_t)((max_query_len + tm - 1) / tm) * d->num_seqs * d->num_kv_heads;
   constexpr int64_t kCtas = 6 * 296;
-  if (pairs >= kCtas) return 2048;
-  const int64_t want = kCtas / pairs, p = ((int64_t)max_context_len + want - 1) / want;
-  return (int)std::min<int64_t>(tree::kPartMax, std::max<int64_t>(128, (p + 63) / 64 * 64));
+  const int64_t fit = std::max<int64_t>(
+      1, (192ll << 20) / ((int64_t)num_tokens * d->num_q_heads * (2 + d->head_dim) * 4));
+  const int64_t want = pairs >= kCtas ? 1 : kCtas / pairs;
+  int64_t p = pairs >= kCtas
+                  ? 2048 : std::max<int64_t>(128, ((int64_t)max_context_len + want - 1) / want);
+  p = std::max<int64_t>(p, ((int64_t)max_context_len + fit - 1) / fit);
+  return (int)std::min<int64_t>((p + 63) / 64 * 64, 1 << 30);
 }
 
 int parts_of(int max_context_len, int part) {
@@ -70,7 +76,8 @@ size_t tree_bytes(const pa_decode_desc* d, int num_tokens, int max_query_len, in
   // either kernel family, so that pa_set_decode_impl does not change it
   int parts = tree_simt_parts(d, num_tokens, max_context_len);
   if (tree_mma(d))
-    parts = std::max(parts, parts_of(max_context_len, tree_mma_part(d, max_query_len, max_context_len)));
+    parts = std::max(parts, parts_of(max_context_len, tree_mma_part(d, num_tokens, max_query_len,
+                                                                    max_context_len)));
   return parts == 1 ? 0 : (size_t)num_tokens * d->num_q_heads * parts * (2 + d->head_dim) * 4;
 }
 
@@ -321,7 +328,7 @@ pa_status paged_attn_tree(const void* q, const void* k_cache, const void* v_cach
   cudaError_t e;
   const bool mma = tree_mma(desc) && g_decode_impl.load(std::memory_order_relaxed) != 1;
   if (mma) {
-    a.part_tokens = tree_mma_part(desc, max_query_len, max_context_len);
+    a.part_tokens = tree_mma_part(desc, num_tokens, max_query_len, max_context_len);
     a.parts = parts_of(max_context_len, a.part_tokens);
   } else {
     a.parts = tree_simt_parts(desc, num_tokens, max_context_len);

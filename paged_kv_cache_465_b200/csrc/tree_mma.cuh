@@ -40,7 +40,7 @@ namespace tree {
 constexpr int kMmaThreads = 128;
 constexpr int kKeys = 64;             // keys of a tile
 constexpr int kMmaDim = 128;
-constexpr int kPartMax = 5120;        // tokens of a part, at most: their block ids stay in shared memory
+constexpr int kPartMax = 5120;        // tokens whose block ids and scales are held at a time
 constexpr int kCombRow = kMmaDim + 4; // floats of a row where the warps join
 
 template <pa_dtype KV, int MT, int WR>
@@ -139,10 +139,11 @@ tree_mma_kernel(const TreeArgs a, int rts) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) flag_error(PA_DEVERR_QUERY);
     return;
   }
-  const int t0 = part * a.part_tokens;
-  if (rt * TM >= n || t0 >= ctx) return;
-  const int t1 = min(ctx, t0 + a.part_tokens), base = ctx - n;
-  const int ntiles = (t1 - t0 + kKeys - 1) / kKeys, rows = min(TM, n - rt * TM);
+  if (rt * TM >= n || (int64_t)part * a.part_tokens >= ctx) return;
+  const int begin = part * a.part_tokens, end = min((int64_t)ctx, (int64_t)begin + a.part_tokens);
+  // the stretch at hand: all of a part but for very long ones
+  int t0 = begin, t1 = min(end, begin + kPartMax), ntiles = (t1 - t0 + kKeys - 1) / kKeys;
+  const int base = ctx - n, rows = min(TM, n - rt * TM);
   const int row0 = q0 + rt * TM;
 
   if (tid < 10) s_odd[tid] = 0;
@@ -160,7 +161,7 @@ tree_mma_kernel(const TreeArgs a, int rts) {
       qx[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
                 ((int64_t)(row0 + r / G) * a.num_q_heads + kvh * G + r % G) * kMmaDim + ch * 8);
   }
-  {
+  auto load_ids = [&]() {
     const int32_t* bt = a.block_tables + (int64_t)s * a.max_blocks_per_seq + t0 / BS;
     const int nb = (t1 - t0 + BS - 1) / BS;
     // up to the last tile's end; what is not there or cannot be read has id -1 and zeros
@@ -187,9 +188,10 @@ tree_mma_kernel(const TreeArgs a, int rts) {
       s_id[i] = p;
       if (i < nb && p < 0) s_odd[9] = 1;
     }
-  }
+  };
+  load_ids();
   __syncthreads();
-  const bool any_bad = s_odd[9] != 0;
+  bool any_bad = s_odd[9] != 0;
 
   // ---- keys: K and V of tile j into stage j % kStages ----
   const uint32_t s0 = tc::smem_u32(smem);
@@ -288,301 +290,312 @@ tree_mma_kernel(const TreeArgs a, int rts) {
       for (int k = 0; k < 4; ++k) o[mt][i][k] = 0.f;
   float vref = 0.f;   // codes: the power of two that P's V scales are relative to
 
+  while (true) {
 #pragma unroll 1
-  for (int j = 0; j < ntiles; ++j) {
-    copies_wait<L::kStages - 2>();
-    __syncthreads();   // tile j is there, and every warp is done with tile j - 1
-    issue(j + L::kStages - 1);
-    const uint32_t sK = s0 + (j % L::kStages) * 2 * L::kTileBytes, sV = sK + L::kTileBytes;
-    const int key0 = t0 + j * kKeys;
-    const bool masked = key0 + kKeys > base || any_bad;
-    uint64_t view[MT * 2];
-    if (masked) {
-      if constexpr (KV != PA_INT8) {
-        // A NaN or infinity in a draft's V row would reach rows that do not see it, as 0 times
-        // itself: it is taken out here and given back at the end to rows that do see it.
-        if (key0 + kKeys > base) {
-          const uint32_t vt = sV - s0;
-          for (int x = tid; x < kKeys * CPR; x += kMmaThreads) {
-            const int key = x / CPR, at = key0 + key;
-            if (at < base || at >= ctx) continue;
-            uint32_t* w = reinterpret_cast<uint32_t*>(smem + vt + key * CPR * 16 + (x % CPR) * 16);
-            bool odd = false;
+    for (int j = 0; j < ntiles; ++j) {
+      copies_wait<L::kStages - 2>();
+      __syncthreads();   // tile j is there, and every warp is done with tile j - 1
+      issue(j + L::kStages - 1);
+      const uint32_t sK = s0 + (j % L::kStages) * 2 * L::kTileBytes, sV = sK + L::kTileBytes;
+      const int key0 = t0 + j * kKeys;
+      const bool masked = key0 + kKeys > base || any_bad;
+      uint64_t view[MT * 2];
+      if (masked) {
+        if constexpr (KV != PA_INT8) {
+          // A NaN or infinity in a draft's V row would reach rows that do not see it, as 0 times
+          // itself: it is taken out here and given back at the end to rows that do see it.
+          if (key0 + kKeys > base) {
+            const uint32_t vt = sV - s0;
+            for (int x = tid; x < kKeys * CPR; x += kMmaThreads) {
+              const int key = x / CPR, at = key0 + key;
+              if (at < base || at >= ctx) continue;
+              uint32_t* w = reinterpret_cast<uint32_t*>(smem + vt + key * CPR * 16 + (x % CPR) * 16);
+              bool odd = false;
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              uint32_t keep = ~0u;
-              if constexpr (QUANT) {
+              for (int i = 0; i < 4; ++i) {
+                uint32_t keep = ~0u;
+                if constexpr (QUANT) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                  if (((w[i] >> (8 * b)) & 0x7fu) == 0x7fu) keep &= ~(0xffu << (8 * b));
-              } else {
-                if ((w[i] & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
-                if ((w[i] & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
+                  for (int b = 0; b < 4; ++b)
+                    if (((w[i] >> (8 * b)) & 0x7fu) == 0x7fu) keep &= ~(0xffu << (8 * b));
+                } else {
+                  if ((w[i] & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+                  if ((w[i] & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
+                }
+                if (keep != ~0u) {
+                  w[i] &= keep;
+                  odd = true;
+                }
               }
-              if (keep != ~0u) {
-                w[i] &= keep;
-                odd = true;
+              if (odd) {
+                atomicOr(&s_odd[(at - base) >> 5], 1u << ((at - base) & 31));
+                s_odd[8] = 1;
               }
             }
-            if (odd) {
-              atomicOr(&s_odd[(at - base) >> 5], 1u << ((at - base) & 31));
-              s_odd[8] = 1;
-            }
-          }
-          __syncthreads();
-        }
-      }
-      uint64_t gone = 0;
-      if (any_bad) {
-#pragma unroll
-        for (int b = 0; b < kKeys / BS; ++b)
-          if (key0 + b * BS < t1 && s_id[j * (kKeys / BS) + b] < 0) gone |= ((1ull << BS) - 1ull) << (b * BS);
-      }
-#pragma unroll
-      for (int i = 0; i < MT * 2; ++i) {
-        const int tok = min((wr * 16 * MT + i * 8 + qr) / G, rows - 1);
-        view[i] = tile_view(a, row0 + tok, key0, base, ctx) & ~gone;
-      }
-    }
-#pragma unroll 1
-    for (int cc = 0; cc < KW / C; ++cc) {
-      const int k0 = wk * KW + cc * C;     // first of the step's keys in the tile
-      if (key0 + k0 >= t1) break;          // none of them exists (a warp's view: uniform)
-      // ---- S ----
-      float sv[MT][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sv[mt][nt][k] = 0.f;
-      if constexpr (!QUANT) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          uint32_t qa[MT][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if constexpr (HOLD) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) qa[mt][k] = qh[mt][kk][k];
-            } else {
-              q_bf16(mt, kk, qa[mt]);
-            }
-          }
-#pragma unroll
-          for (int np = 0; np < NT / 2; ++np) {
-            uint32_t b[4];
-            const int key = k0 + np * 16 + (lane & 7) + ((lane >> 4) << 3);
-            const int c = kk * 2 + ((lane >> 3) & 1);
-            tc::ldsm_x4(sK + key * 256 + ((c ^ (key & 7)) << 4), b);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              tc::mma16816<false>(sv[mt][2 * np], qa[mt], b[0], b[1]);
-              tc::mma16816<false>(sv[mt][2 * np + 1], qa[mt], b[2], b[3]);
-            }
+            __syncthreads();
           }
         }
-      } else {
+        uint64_t gone = 0;
+        if (any_bad) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 kc[NT];
+          for (int b = 0; b < kKeys / BS; ++b)
+            if (key0 + b * BS < t1 && s_id[j * (kKeys / BS) + b] < 0) gone |= ((1ull << BS) - 1ull) << (b * BS);
+        }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int key = k0 + nt * 8 + qr;
-            kc[nt] = lds128(sK + key * 128 + (((t + 4 * h) ^ (4 * (key & 1))) << 4));
-          }
+        for (int i = 0; i < MT * 2; ++i) {
+          const int tok = min((wr * 16 * MT + i * 8 + qr) / G, rows - 1);
+          view[i] = tile_view(a, row0 + tok, key0, base, ctx) & ~gone;
+        }
+      }
+#pragma unroll 1
+      for (int cc = 0; cc < KW / C; ++cc) {
+        const int k0 = wk * KW + cc * C;     // first of the step's keys in the tile
+        if (key0 + k0 >= t1) break;          // none of them exists (a warp's view: uniform)
+        // ---- S ----
+        float sv[MT][NT][4];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            uint32_t qa[MT][2][4];
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sv[mt][nt][k] = 0.f;
+        if constexpr (!QUANT) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            uint32_t qa[MT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               if constexpr (HOLD) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  qa[mt][0][k] = qh[mt][4 * h + 2 * b][k];
-                  qa[mt][1][k] = qh[mt][4 * h + 2 * b + 1][k];
-                }
+                for (int k = 0; k < 4; ++k) qa[mt][k] = qh[mt][kk][k];
               } else {
-                q_f16(mt, h, b, qa[mt][0], qa[mt][1]);
+                q_bf16(mt, kk, qa[mt]);
               }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t zc = 0;
-              if constexpr (KV == PA_INT8) {
-                const float z = 1152.f + (float)s_kz[(j * kKeys + k0 + nt * 8) / BS];
-                zc = pack_f16x2(z, z);
+            for (int np = 0; np < NT / 2; ++np) {
+              uint32_t b[4];
+              const int key = k0 + np * 16 + (lane & 7) + ((lane >> 4) << 3);
+              const int c = kk * 2 + ((lane >> 3) & 1);
+              tc::ldsm_x4(sK + key * 256 + ((c ^ (key & 7)) << 4), b);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                tc::mma16816<false>(sv[mt][2 * np], qa[mt], b[0], b[1]);
+                tc::mma16816<false>(sv[mt][2 * np + 1], qa[mt], b[2], b[3]);
               }
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t w = b ? (e ? kc[nt].w : kc[nt].z) : (e ? kc[nt].y : kc[nt].x);
-                uint32_t b0, b1;
-                if constexpr (KV == PA_INT8) {
-                  const uint32_t u = w ^ 0x80808080u;
-                  b0 = tc::i8x2_to_f16x2(u, 0x4140, zc);
-                  b1 = tc::i8x2_to_f16x2(u, 0x4342, zc);
-                } else {
-                  b0 = e4m3x2_to_f16x2((uint16_t)(w & 0xffffu));
-                  b1 = e4m3x2_to_f16x2((uint16_t)(w >> 16));
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) tc::mma16816<true>(sv[mt][nt], qa[mt][e], b0, b1);
-              }
-            }
-          }
-        }
-      }
-      // ---- softmax ----
-      float ks[NT], vs[NT], beta = 1.f;
-      if constexpr (QUANT) {
-        float vmax = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int b = (j * kKeys + k0 + nt * 8) / BS;
-          ks[nt] = s_ks[b];
-          vs[nt] = s_vs[b];
-          vmax = fmaxf(vmax, fabsf(vs[nt]));
-        }
-        if (vmax > vref) {
-          // the next power of two, within a range whose reciprocal is one too
-          const int e = max(27, min(227, (int)((__float_as_uint(vmax) >> 23) & 0xff) + 1));
-          const float up = __uint_as_float((uint32_t)e << 23);
-          beta = vref > 0.f ? fminf(vref / up, 1.f) : 1.f;
-          vref = fmaxf(vref, up);
-        }
-        const float rvs = vref > 0.f ? 128.f / vref : 0.f;   // 0: every V scale so far is
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) vs[nt] *= rvs;
-      }
-      uint32_t pf[MT][NT / 2][4];
-      // P against the standing reference, without looking for the maximum: right when no lane's
-      // sum passes 2^8 (a score that outgrew the reference, or is no number, makes one)
-      auto weights = [&](int i, float f0, bool scaled) {
-        const float ref = m[i] == -INFINITY && scaled ? 0.f : -m[i];
-        float sum = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float f = scaled ? 1.f : QUANT ? f0 * ks[nt] : f0;
-          float p0 = fast_exp2(fmaf(sv[i >> 1][nt][2 * (i & 1)], f, ref));
-          float p1 = fast_exp2(fmaf(sv[i >> 1][nt][2 * (i & 1) + 1], f, ref));
-          sum += p0 + p1;
-          if constexpr (QUANT) {   // P carries its block's V scale; a key that is not seen, none
-            p0 = scaled && p0 == 0.f ? 0.f : p0 * vs[nt];
-            p1 = scaled && p1 == 0.f ? 0.f : p1 * vs[nt];
-          }
-          pf[i >> 1][nt >> 1][2 * (nt & 1) + (i & 1)] = QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-        }
-        return sum;
-      };
-      bool fast = false;
-      if (!masked && beta == 1.f) {
-        float sum[MT * 2];
-        bool good = true;
-#pragma unroll
-        for (int i = 0; i < MT * 2; ++i) {
-          sum[i] = weights(i, sl2[i], false);
-          good = good && sum[i] <= 256.f;
-        }
-        fast = __all_sync(0xffffffffu, good);
-        if (fast) {
-#pragma unroll
-          for (int i = 0; i < MT * 2; ++i) l[i] += sum[i];
-        }
-      }
-      if (!fast) {
-        float alpha[MT * 2];
-        bool grown = beta != 1.f;
-#pragma unroll
-        for (int i = 0; i < MT * 2; ++i) {
-          const uint32_t v = masked ? (uint32_t)(view[i] >> (k0 + 2 * t)) : ~0u;
-          float mx = m[i];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float f = QUANT ? sl2[i] * ks[nt] : sl2[i];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = sv[i >> 1][nt][2 * (i & 1) + e];
-              x *= f;
-              if (masked && !((v >> (nt * 8 + e)) & 1u)) x = -INFINITY;
-              mx = fmaxf(mx, x);
-            }
-          }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          alpha[i] = 1.f;
-          if (mx > m[i] + 8.f) {   // lazy: P stays at or below 2^8 otherwise
-            alpha[i] = fast_exp2(m[i] - mx);
-            m[i] = mx;
-            grown = true;
-          }
-        }
-        if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[mt][i][k] *= alpha[mt * 2 + (k >> 1)] * beta;
-        }
-#pragma unroll
-        for (int i = 0; i < MT * 2; ++i) l[i] = l[i] * alpha[i] + weights(i, 1.f, true);
-      }
-      // ---- O += P V ----
-#pragma unroll
-      for (int kp = 0; kp < NT / 2; ++kp) {
-        const int key = k0 + kp * 16 + (lane & 15);
-        uint32_t z0 = 0, z1 = 0;
-        if constexpr (KV == PA_INT8) {
-          const int b = (j * kKeys + k0 + kp * 16) / BS;
-          const float f0 = 1152.f + (float)s_vz[b];
-          const float f1 = 1152.f + (float)s_vz[BS == 8 ? b + 1 : b];
-          z0 = pack_f16x2(f0, f0);
-          z1 = pack_f16x2(f1, f1);
-        }
-        if constexpr (!QUANT) {
-#pragma unroll
-          for (int cb = 0; cb < 8; ++cb) {   // 16 channels
-            uint32_t b[4];
-            tc::ldsm_x4_t(sV + key * 256 + (((cb * 2 + (lane >> 4)) ^ (key & 7)) << 4), b);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              tc::mma16816<false>(o[mt][2 * cb], pf[mt][kp], b[0], b[1]);
-              tc::mma16816<false>(o[mt][2 * cb + 1], pf[mt][kp], b[2], b[3]);
             }
           }
         } else {
 #pragma unroll
-          for (int cb = 0; cb < 4; ++cb) {   // 32 channels
-            uint32_t w[4];   // (keys 0-7, 8-15) x (channels 0-15, 16-31); lane: two keys, two channels
-            tc::ldsm_x4_t(sV + key * 128 + (((cb * 2 + (lane >> 4)) ^ (key & 7)) << 4), w);
+          for (int h = 0; h < 2; ++h) {
+            uint4 kc[NT];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t ev[2], od[2];   // the even and the odd channel of both keys
+            for (int nt = 0; nt < NT; ++nt) {
+              const int key = k0 + nt * 8 + qr;
+              kc[nt] = lds128(sK + key * 128 + (((t + 4 * h) ^ (4 * (key & 1))) << 4));
+            }
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t u = __byte_perm(w[2 * x + y], 0, 0x3120);
-                if constexpr (KV == PA_INT8) {
-                  const uint32_t ub = u ^ 0x80808080u;
-                  ev[y] = tc::i8x2_to_f16x2(ub, 0x4140, y ? z1 : z0);
-                  od[y] = tc::i8x2_to_f16x2(ub, 0x4342, y ? z1 : z0);
+            for (int b = 0; b < 2; ++b) {
+              uint32_t qa[MT][2][4];
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                if constexpr (HOLD) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    qa[mt][0][k] = qh[mt][4 * h + 2 * b][k];
+                    qa[mt][1][k] = qh[mt][4 * h + 2 * b + 1][k];
+                  }
                 } else {
-                  ev[y] = e4m3x2_to_f16x2((uint16_t)(u & 0xffffu));
-                  od[y] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
+                  q_f16(mt, h, b, qa[mt][0], qa[mt][1]);
                 }
               }
 #pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                uint32_t zc = 0;
+                if constexpr (KV == PA_INT8) {
+                  const float z = 1152.f + (float)s_kz[(j * kKeys + k0 + nt * 8) / BS];
+                  zc = pack_f16x2(z, z);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t w = b ? (e ? kc[nt].w : kc[nt].z) : (e ? kc[nt].y : kc[nt].x);
+                  uint32_t b0, b1;
+                  if constexpr (KV == PA_INT8) {
+                    const uint32_t u = w ^ 0x80808080u;
+                    b0 = tc::i8x2_to_f16x2(u, 0x4140, zc);
+                    b1 = tc::i8x2_to_f16x2(u, 0x4342, zc);
+                  } else {
+                    b0 = e4m3x2_to_f16x2((uint16_t)(w & 0xffffu));
+                    b1 = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+                  }
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) tc::mma16816<true>(sv[mt][nt], qa[mt][e], b0, b1);
+                }
+              }
+            }
+          }
+        }
+        // ---- softmax ----
+        float ks[NT], vs[NT], beta = 1.f;
+        if constexpr (QUANT) {
+          float vmax = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int b = (j * kKeys + k0 + nt * 8) / BS;
+            ks[nt] = s_ks[b];
+            vs[nt] = s_vs[b];
+            vmax = fmaxf(vmax, fabsf(vs[nt]));
+          }
+          if (vmax > vref) {
+            // the next power of two, within a range whose reciprocal is one too
+            const int e = max(27, min(227, (int)((__float_as_uint(vmax) >> 23) & 0xff) + 1));
+            const float up = __uint_as_float((uint32_t)e << 23);
+            beta = vref > 0.f ? fminf(vref / up, 1.f) : 1.f;
+            vref = fmaxf(vref, up);
+          }
+          const float rvs = vref > 0.f ? 128.f / vref : 0.f;   // 0: every V scale so far is
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) vs[nt] *= rvs;
+        }
+        uint32_t pf[MT][NT / 2][4];
+        // P against the standing reference, without looking for the maximum: right when no lane's
+        // sum passes 2^8 (a score that outgrew the reference, or is no number, makes one)
+        auto weights = [&](int i, float f0, bool scaled) {
+          const float ref = m[i] == -INFINITY && scaled ? 0.f : -m[i];
+          float sum = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float f = scaled ? 1.f : QUANT ? f0 * ks[nt] : f0;
+            float p0 = fast_exp2(fmaf(sv[i >> 1][nt][2 * (i & 1)], f, ref));
+            float p1 = fast_exp2(fmaf(sv[i >> 1][nt][2 * (i & 1) + 1], f, ref));
+            sum += p0 + p1;
+            if constexpr (QUANT) {   // P carries its block's V scale; a key that is not seen, none
+              p0 = scaled && p0 == 0.f ? 0.f : p0 * vs[nt];
+              p1 = scaled && p1 == 0.f ? 0.f : p1 * vs[nt];
+            }
+            pf[i >> 1][nt >> 1][2 * (nt & 1) + (i & 1)] = QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+          return sum;
+        };
+        bool fast = false;
+        if (!masked && beta == 1.f) {
+          float sum[MT * 2];
+          bool good = true;
+#pragma unroll
+          for (int i = 0; i < MT * 2; ++i) {
+            sum[i] = weights(i, sl2[i], false);
+            good = good && sum[i] <= 256.f;
+          }
+          fast = __all_sync(0xffffffffu, good);
+          if (fast) {
+#pragma unroll
+            for (int i = 0; i < MT * 2; ++i) l[i] += sum[i];
+          }
+        }
+        if (!fast) {
+          float alpha[MT * 2];
+          bool grown = beta != 1.f;
+#pragma unroll
+          for (int i = 0; i < MT * 2; ++i) {
+            const uint32_t v = masked ? (uint32_t)(view[i] >> (k0 + 2 * t)) : ~0u;
+            float mx = m[i];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float f = QUANT ? sl2[i] * ks[nt] : sl2[i];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& x = sv[i >> 1][nt][2 * (i & 1) + e];
+                x *= f;
+                if (masked && !((v >> (nt * 8 + e)) & 1u)) x = -INFINITY;
+                mx = fmaxf(mx, x);
+              }
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            alpha[i] = 1.f;
+            if (mx > m[i] + 8.f) {   // lazy: P stays at or below 2^8 otherwise
+              alpha[i] = fast_exp2(m[i] - mx);
+              m[i] = mx;
+              grown = true;
+            }
+          }
+          if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[mt][i][k] *= alpha[mt * 2 + (k >> 1)] * beta;
+          }
+#pragma unroll
+          for (int i = 0; i < MT * 2; ++i) l[i] = l[i] * alpha[i] + weights(i, 1.f, true);
+        }
+        // ---- O += P V ----
+#pragma unroll
+        for (int kp = 0; kp < NT / 2; ++kp) {
+          const int key = k0 + kp * 16 + (lane & 15);
+          uint32_t z0 = 0, z1 = 0;
+          if constexpr (KV == PA_INT8) {
+            const int b = (j * kKeys + k0 + kp * 16) / BS;
+            const float f0 = 1152.f + (float)s_vz[b];
+            const float f1 = 1152.f + (float)s_vz[BS == 8 ? b + 1 : b];
+            z0 = pack_f16x2(f0, f0);
+            z1 = pack_f16x2(f1, f1);
+          }
+          if constexpr (!QUANT) {
+#pragma unroll
+            for (int cb = 0; cb < 8; ++cb) {   // 16 channels
+              uint32_t b[4];
+              tc::ldsm_x4_t(sV + key * 256 + (((cb * 2 + (lane >> 4)) ^ (key & 7)) << 4), b);
+#pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                tc::mma16816<true>(o[mt][4 * cb + 2 * x], pf[mt][kp], ev[0], ev[1]);
-                tc::mma16816<true>(o[mt][4 * cb + 2 * x + 1], pf[mt][kp], od[0], od[1]);
+                tc::mma16816<false>(o[mt][2 * cb], pf[mt][kp], b[0], b[1]);
+                tc::mma16816<false>(o[mt][2 * cb + 1], pf[mt][kp], b[2], b[3]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {   // 32 channels
+              uint32_t w[4];   // (keys 0-7, 8-15) x (channels 0-15, 16-31); lane: two keys, two channels
+              tc::ldsm_x4_t(sV + key * 128 + (((cb * 2 + (lane >> 4)) ^ (key & 7)) << 4), w);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t ev[2], od[2];   // the even and the odd channel of both keys
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t u = __byte_perm(w[2 * x + y], 0, 0x3120);
+                  if constexpr (KV == PA_INT8) {
+                    const uint32_t ub = u ^ 0x80808080u;
+                    ev[y] = tc::i8x2_to_f16x2(ub, 0x4140, y ? z1 : z0);
+                    od[y] = tc::i8x2_to_f16x2(ub, 0x4342, y ? z1 : z0);
+                  } else {
+                    ev[y] = e4m3x2_to_f16x2((uint16_t)(u & 0xffffu));
+                    od[y] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
+                  }
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  tc::mma16816<true>(o[mt][4 * cb + 2 * x], pf[mt][kp], ev[0], ev[1]);
+                  tc::mma16816<true>(o[mt][4 * cb + 2 * x + 1], pf[mt][kp], od[0], od[1]);
+                }
               }
             }
           }
         }
       }
     }
+    copies_wait<0>();
+    __syncthreads();   // stages and Q are free: the next stretch's keys, or the warps join there
+    if (t1 == end) break;
+    t0 = t1;
+    t1 = min(end, t0 + kPartMax);
+    ntiles = (t1 - t0 + kKeys - 1) / kKeys;
+    load_ids();
+    __syncthreads();
+    any_bad = s_odd[9] != 0;
+#pragma unroll 1
+    for (int j = 0; j < L::kStages - 1; ++j) issue(j);
   }
-  copies_wait<0>();
-  __syncthreads();   // stages and Q are free: the warps join there
 
   float* comb = reinterpret_cast<float*>(smem);   // [WK][R][kCombRow]
   const float unit = QUANT ? vref * (1.f / 128.f) : 1.f;
@@ -634,10 +647,11 @@ tree_mma_kernel(const TreeArgs a, int rts) {
 #pragma unroll 1
       for (int d = 0; d < n; ++d) {
         const int key = base + d;
-        if (key < t0 || key >= t1 || !((s_odd[d >> 5] >> (d & 31)) & 1u) ||
+        if (key < begin || key >= end || !((s_odd[d >> 5] >> (d & 31)) & 1u) ||
             !((a.tree_mask[trow * a.mask_words + (d >> 5)] >> (d & 31)) & 1u))
           continue;
-        const int64_t at = (((int64_t)s_id[(key - t0) / BS] * Hkv + kvh) * BS + key % BS) * kMmaDim + c;
+        const int64_t blk = a.block_tables[(int64_t)s * a.max_blocks_per_seq + key / BS];
+        const int64_t at = ((blk * Hkv + kvh) * BS + key % BS) * kMmaDim + c;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if constexpr (!QUANT) {

@@ -674,6 +674,16 @@ def test_tree_lengths_far_below_the_longest_allowed(pa, impl, kv):
     t.check(pa, impl)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("new", [5, 40])
+def test_tree_long_parts(pa, kv, new):
+    """A step with very many (padding) rows does not cut its contexts: a CTA takes a long one
+    stretch by stretch, with drafts that lie across a stretch's end."""
+    t = Tree(25, [12000, 5100, 5120, 40], [new] * 4, 4, 1, 128, 16, kv, pad=100000)
+    assert t.workspace(pa).numel() == 16
+    t.check(pa)
+
+
 @pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("kv", ["fp8", "int8"])
 def test_tree_scales_of_either_sign_that_differ_between_blocks(pa, impl, kv):
