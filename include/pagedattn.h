@@ -330,7 +330,10 @@ pa_status copy_blocks(void* k_cache, void* v_cache, float* k_scales, float* v_sc
  * parent is recorded (PA_DEVERR_TREE) and its row treated as one right behind the context;
  * a row whose block id is outside [0, num_blocks) gets slot -1 (PA_DEVERR_BLOCK_ID).
  * Every output but block_tables is written in full; none may overlap an input. The same
- * call on the same inputs gives the same outputs.
+ * call on the same inputs gives the same outputs. That holds for num_seqs = 0 too (an idle
+ * step: no rows, every slot -1, the queue passed on); the buffers of one entry per sequence
+ * may then be NULL. Only a call of no sequences that has new_lens and no context_lens is
+ * taken for no batch at all: PA_OK, nothing is written.
  */
 pa_status paged_build_step(const int32_t* context_lens, const int32_t* new_lens,
                            const int32_t* blocks_held, const int32_t* parents,
@@ -351,7 +354,9 @@ pa_status paged_build_step(const int32_t* context_lens, const int32_t* new_lens,
  * they are (blocks_held_out says how many count). Buffers as in paged_build_step;
  * free_blocks is written. All or nothing: a negative length, held blocks outside [0,
  * max_blocks_per_seq] (PA_DEVERR_CONTEXT) or a queue that would not hold them
- * (PA_DEVERR_QUEUE) change nothing.
+ * (PA_DEVERR_QUEUE) change nothing but the outputs, which are as the inputs. num_seqs = 0
+ * passes the queue on, with buffers as in paged_build_step (no batch at all: blocks_held
+ * and no keep_lens).
  */
 pa_status paged_release_blocks(const int32_t* keep_lens, const int32_t* blocks_held,
                                const int32_t* block_tables, int32_t* free_blocks,

@@ -24,11 +24,11 @@ struct Span {
 // Whether no output shares memory with another buffer (absent ones have no pointer).
 bool apart(std::initializer_list<Span> all) {
   for (const Span& a : all) {
-    if (!a.out || a.p == nullptr) continue;
+    if (!a.out || a.p == nullptr || a.bytes == 0) continue;
     const char* a0 = static_cast<const char*>(a.p);
     for (const Span& b : all) {
       const char* b0 = static_cast<const char*>(b.p);
-      if (&a != &b && b0 != nullptr && a0 < b0 + b.bytes && b0 < a0 + a.bytes) return false;
+      if (&a != &b && b0 != nullptr && b.bytes > 0 && a0 < b0 + b.bytes && b0 < a0 + a.bytes) return false;
     }
   }
   return true;
@@ -145,9 +145,14 @@ pa_status paged_build_step(const int32_t* context_lens, const int32_t* new_lens,
       (int64_t)max_blocks_per_seq * block_size > INT32_MAX)
     return PA_ERR_INVALID;
   if (tree_mask && (mask_words < 1 || mask_words > step::kMaxWords)) return PA_ERR_INVALID;
-  if (num_seqs == 0) return PA_OK;
-  if (!context_lens || !new_lens || !blocks_held || !block_tables || !free_blocks ||
-      !queue_state || !total_lens || !query_start || !blocks_held_out || !queue_state_out ||
+  if (num_seqs == 0) {
+    if (!context_lens && new_lens) return PA_OK;  // no batch at all
+  } else if (!context_lens || !new_lens || !blocks_held || !block_tables || !total_lens ||
+             !blocks_held_out) {
+    return PA_ERR_INVALID;
+  }
+  // an idle step's outputs are written like any other's
+  if (!free_blocks || !queue_state || !query_start || !queue_state_out ||
       (max_tokens > 0 && !slot_mapping))
     return PA_ERR_INVALID;
   // every CTA reads the inputs while the first writes the outputs
@@ -180,10 +185,12 @@ pa_status paged_release_blocks(const int32_t* keep_lens, const int32_t* blocks_h
   if (num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq <= 0 || block_size <= 0 ||
       free_capacity <= 0)
     return PA_ERR_INVALID;
-  if (num_seqs == 0) return PA_OK;
-  if (!keep_lens || !blocks_held || !block_tables || !free_blocks || !queue_state ||
-      !blocks_held_out || !queue_state_out)
+  if (num_seqs == 0) {
+    if (!keep_lens && blocks_held) return PA_OK;  // no batch at all
+  } else if (!keep_lens || !blocks_held || !block_tables || !blocks_held_out) {
     return PA_ERR_INVALID;
+  }
+  if (!free_blocks || !queue_state || !queue_state_out) return PA_ERR_INVALID;
   const int64_t S4 = 4 * (int64_t)num_seqs;
   if (!apart({{keep_lens, S4, false}, {blocks_held, S4, false},
               {block_tables, S4 * max_blocks_per_seq, false},
@@ -195,7 +202,8 @@ pa_status paged_release_blocks(const int32_t* keep_lens, const int32_t* blocks_h
   const step::ReleaseArgs a{keep_lens, blocks_held, block_tables, free_blocks, queue_state,
                             blocks_held_out, queue_state_out, status, num_seqs,
                             max_blocks_per_seq, block_size, free_capacity, per};
-  const cudaError_t e = launch_pdl(step::release_blocks_kernel, dim3((num_seqs + per - 1) / per),
+  const cudaError_t e = launch_pdl(step::release_blocks_kernel,
+                                   dim3(std::max(1, (num_seqs + per - 1) / per)),
                                    dim3(step::kReleaseThreads), 0, as_stream(stream), a);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -125,6 +125,54 @@ def test_build_step_whole_queue_and_no_tokens(pa):
     assert not o["positions"].any() and not o["tree_mask"].any()
 
 
+@pytest.mark.parametrize("rows", [0, 5, 2500])
+@pytest.mark.parametrize("words", [0, 2])
+def test_build_step_of_no_sequences(pa, rows, words):
+    """An idle step of fixed width writes every output: no slot, no rows, the queue as it was."""
+    none = np.zeros(0)
+    bt, o = build(pa, none, none, none, np.zeros((0, 3)), [4, 1, 0, 2], [3, 2], 16, 6, rows, words=words)
+    assert pa.device_error() == 0 and o["status"].tolist() == [0]
+    assert o["query_start"].tolist() == [0] and o["queue_state_out"].tolist() == [3, 2]
+    assert (o["slot_mapping"] == -1).all() and not o["positions"].any()
+    assert not words or not o["tree_mask"].any()
+    _, o = build(pa, none, none, none, np.zeros((0, 3)), [4, 1, 0, 2], [4, 2], 16, 6, rows, words=words)
+    assert pa.device_error() == 0x200 and o["status"].tolist() == [0x200]
+    assert (o["slot_mapping"] == -1).all() and o["queue_state_out"].tolist() == [4, 2]
+
+
+def test_release_blocks_of_no_sequences(pa):
+    """The queue is passed on: a program that chains queue states does not go back to an old one."""
+    ring, out, status = cuda([4, 1, 0, 2]), cuda([-7, -7]), cuda([-7])
+    pa.release_blocks(cuda([]), cuda([]), cuda(np.zeros((0, 3))), ring, cuda([3, 2]), block_size=16,
+                      blocks_held_out=cuda([]), queue_state_out=out, status=status)
+    assert out.tolist() == [3, 2] and status.tolist() == [0] and ring.tolist() == [4, 1, 0, 2]
+    assert pa.device_error() == 0
+
+
+def test_an_idle_step_writes_nothing_to_the_cache(pa):
+    """A fixed-width step of two sequences, then one of none into the same buffers: the second
+    step's rows reach no cache row."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = lambda h: torch.randn(4, h, 64, device="cuda", generator=g).bfloat16()  # noqa: E731
+    kc, vc = (torch.randn(6, 2, 16, 64, device="cuda", generator=g).bfloat16() for _ in range(2))
+    o = dict(query_start=cuda(np.full(3, -7)), queue_state_out=cuda([-7, -7]),
+             slot_mapping=cuda(np.full(4, -7), torch.int64), positions=cuda(np.full(4, -7)))
+
+    def step(S, queue):
+        new = {n: cuda(np.full(S, -7)) for n in ("total_lens", "blocks_held_out")}
+        pa.build_step(cuda([16, 3][:S]), cuda([1, 2][:S]), cuda([1, 1][:S]), cuda(np.array([[3, -1], [5, -1]])[:S]),
+                      cuda([4, 1, 0, 2]), queue, block_size=16, num_blocks=6, **new,
+                      **dict(o, query_start=o["query_start"][:S + 1]))
+        pa.rotary_and_cache(x(4), x(2), x(2), x(4), kc, vc, o["positions"], o["slot_mapping"],
+                            torch.ones(32, device="cuda"))
+    step(2, cuda([3, 2]))
+    assert o["slot_mapping"].tolist() == [32, 83, 84, -1] and o["queue_state_out"].tolist() == [0, 1]
+    before, queue = (kc.clone(), vc.clone()), o["queue_state_out"].clone()
+    step(0, queue)
+    assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
+    assert torch.equal(o["queue_state_out"], queue) and pa.device_error() == 0
+
+
 @pytest.mark.parametrize("why,bit", [("blocks", 0x100), ("rows", 0x20), ("one_too_long", 0x80), ("queue_head", 0x200),
                                      ("queue_count", 0x200), ("negative", 0x8), ("table", 0x8),
                                      ("held", 0x8), ("wide", 0x80)])

@@ -253,6 +253,32 @@ def test_refusals_without_a_device(pa):
     assert compact(S=0, ptr=nul) == pa.PA_OK
 
 
+def test_idle_steps_are_checked_too(pa):
+    """No sequences: the buffers that are read or written all the same have to be there, and apart."""
+    nul = ctypes.c_void_p(0)
+    at = [ctypes.c_void_p(4096 * (i + 1)) for i in range(20)]
+
+    def build(rows=8, **kw):
+        p = [nul] * 5 + at[5:7] + [nul] + [at[8], nul] + at[10:15]   # per-sequence buffers absent
+        for k, v in kw.items():
+            p[int(k[1:])] = v
+        return pa._lib.paged_build_step(*p[:7], 0, 4, 16, 8, 8, rows, 2, *p[7:15], nul)
+    for i in (5, 6, 8, 10, 11):
+        assert build(**{f"p{i}": nul}) == pa.PA_ERR_INVALID, i
+    for i, j in ((10, 6), (8, 5), (11, 6), (14, 12), (13, 11)):
+        assert build(**{f"p{i}": at[j]}) == pa.PA_ERR_INVALID, (i, j)
+
+    def release(**kw):
+        p = [nul] * 3 + at[3:5] + [nul] + at[6:8]
+        for k, v in kw.items():
+            p[int(k[1:])] = v
+        return pa._lib.paged_release_blocks(*p[:5], 0, 4, 16, 8, *p[5:8], nul)
+    for i in (3, 4, 6):
+        assert release(**{f"p{i}": nul}) == pa.PA_ERR_INVALID, i
+    for i, j in ((6, 4), (7, 3), (7, 6)):
+        assert release(**{f"p{i}": at[j]}) == pa.PA_ERR_INVALID, (i, j)
+
+
 def test_tree_workspace_does_not_grow_with_the_context(pa):
     """Contexts are cut into no more parts than fill the GPU, and on the tensor cores into no more
     than whose results fit 192 MB."""
