@@ -27,8 +27,9 @@
 // Types: a bf16 cache is multiplied as it is, with P rounded to bf16. Codes of one byte become
 // f16 in registers: E4M3 values and code - zero are exact. Q rows are brought to [2^14, 2^15) by
 // a power of two each, which bf16's eight bits survive down to 2^-28 of the row's largest
-// element. P carries V scale / v_ref * 2^7, v_ref a power of two no smaller than any |V scale| so
-// far: at most 2^15, and f16 holds it to 11 bits down to 2^-21 of the largest.
+// element. P carries V scale / v_ref * 2^7, v_ref a power of two, for each row no smaller than any
+// |V scale| of the keys that it has seen: at most 2^15, and f16 holds it to 11 bits down to 2^-21
+// of the largest. Scales of keys that a row does not see, infinite ones too, do not reach it.
 #pragma once
 
 #include "decode_tc.cuh"
@@ -288,7 +289,11 @@ tree_mma_kernel(const TreeArgs a, int rts) {
     for (int i = 0; i < 16; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[mt][i][k] = 0.f;
-  float vref = 0.f;   // codes: the power of two that P's V scales are relative to
+  // codes: the power of two that a row's V scales are relative to. Rows differ only from the first
+  // key on that some of them do not see: in unmasked tiles, which come before, all are alike.
+  float vref[MT * 2];
+#pragma unroll
+  for (int i = 0; i < MT * 2; ++i) vref[i] = 0.f;
 
   while (true) {
 #pragma unroll 1
@@ -436,9 +441,9 @@ tree_mma_kernel(const TreeArgs a, int rts) {
           }
         }
         // ---- softmax ----
-        float ks[NT], vs[NT], beta = 1.f;
+        float ks[NT], vs[NT], rv[MT * 2];
         if constexpr (QUANT) {
-          float vmax = 0.f;
+          float vmax = 0.f, seen[MT * 2];   // the largest |V scale|, of all keys and of a row's
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const int b = (j * kKeys + k0 + nt * 8) / BS;
@@ -446,16 +451,40 @@ tree_mma_kernel(const TreeArgs a, int rts) {
             vs[nt] = s_vs[b];
             vmax = fmaxf(vmax, fabsf(vs[nt]));
           }
-          if (vmax > vref) {
-            // the next power of two, within a range whose reciprocal is one too
-            const int e = max(27, min(227, (int)((__float_as_uint(vmax) >> 23) & 0xff) + 1));
-            const float up = __uint_as_float((uint32_t)e << 23);
-            beta = vref > 0.f ? fminf(vref / up, 1.f) : 1.f;
-            vref = fmaxf(vref, up);
-          }
-          const float rvs = vref > 0.f ? 128.f / vref : 0.f;   // 0: every V scale so far is
+          bool up = false;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) vs[nt] *= rvs;
+          for (int i = 0; i < MT * 2; ++i) {
+            seen[i] = vmax;
+            if (masked) {
+              const uint32_t v = (uint32_t)(view[i] >> k0);
+              seen[i] = 0.f;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                if ((v >> (8 * nt)) & 0xffu) seen[i] = fmaxf(seen[i], fabsf(vs[nt]));
+            }
+            up = up || seen[i] > vref[i];
+          }
+          if (__any_sync(0xffffffffu, up)) {
+            // The next power of two, within a range in which 2^7 over it is one too; what was
+            // summed against a lower one is scaled down.
+#pragma unroll
+            for (int i = 0; i < MT * 2; ++i) {
+              if (!(seen[i] > vref[i])) continue;
+              const int e = max(8, min(253, (int)((__float_as_uint(seen[i]) >> 23) & 0xff) + 1));
+              const float now = fmaxf(vref[i], __uint_as_float((uint32_t)e << 23));
+              const float down = vref[i] / now;
+              vref[i] = now;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                o[i >> 1][k][2 * (i & 1)] *= down;
+                o[i >> 1][k][2 * (i & 1) + 1] *= down;
+              }
+            }
+          }
+          // 2^7 / v_ref by its exponent; 0: every V scale so far is
+#pragma unroll
+          for (int i = 0; i < MT * 2; ++i)
+            rv[i] = vref[i] > 0.f ? __uint_as_float((261u << 23) - __float_as_uint(vref[i])) : 0.f;
         }
         uint32_t pf[MT][NT / 2][4];
         // P against the standing reference, without looking for the maximum: right when no lane's
@@ -470,15 +499,16 @@ tree_mma_kernel(const TreeArgs a, int rts) {
             float p1 = fast_exp2(fmaf(sv[i >> 1][nt][2 * (i & 1) + 1], f, ref));
             sum += p0 + p1;
             if constexpr (QUANT) {   // P carries its block's V scale; a key that is not seen, none
-              p0 = scaled && p0 == 0.f ? 0.f : p0 * vs[nt];
-              p1 = scaled && p1 == 0.f ? 0.f : p1 * vs[nt];
+              const float w = vs[nt] * rv[scaled ? i : 0];   // rows are alike in unmasked tiles
+              p0 = scaled && p0 == 0.f ? 0.f : p0 * w;
+              p1 = scaled && p1 == 0.f ? 0.f : p1 * w;
             }
             pf[i >> 1][nt >> 1][2 * (nt & 1) + (i & 1)] = QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           }
           return sum;
         };
         bool fast = false;
-        if (!masked && beta == 1.f) {
+        if (!masked) {
           float sum[MT * 2];
           bool good = true;
 #pragma unroll
@@ -494,7 +524,7 @@ tree_mma_kernel(const TreeArgs a, int rts) {
         }
         if (!fast) {
           float alpha[MT * 2];
-          bool grown = beta != 1.f;
+          bool grown = false;
 #pragma unroll
           for (int i = 0; i < MT * 2; ++i) {
             const uint32_t v = masked ? (uint32_t)(view[i] >> (k0 + 2 * t)) : ~0u;
@@ -525,7 +555,7 @@ tree_mma_kernel(const TreeArgs a, int rts) {
 #pragma unroll
               for (int i = 0; i < 16; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[mt][i][k] *= alpha[mt * 2 + (k >> 1)] * beta;
+                for (int k = 0; k < 4; ++k) o[mt][i][k] *= alpha[mt * 2 + (k >> 1)];
           }
 #pragma unroll
           for (int i = 0; i < MT * 2; ++i) l[i] = l[i] * alpha[i] + weights(i, 1.f, true);
@@ -598,7 +628,6 @@ tree_mma_kernel(const TreeArgs a, int rts) {
   }
 
   float* comb = reinterpret_cast<float*>(smem);   // [WK][R][kCombRow]
-  const float unit = QUANT ? vref * (1.f / 128.f) : 1.f;
 #pragma unroll
   for (int i = 0; i < MT * 2; ++i) {
     float x = l[i];
@@ -611,6 +640,7 @@ tree_mma_kernel(const TreeArgs a, int rts) {
     }
     float* d = comb + (wk * R + r) * kCombRow;
     const int k = 2 * (i & 1);
+    const float unit = QUANT ? vref[i] * (1.f / 128.f) : 1.f;
 #pragma unroll
     for (int cb = 0; cb < 8; ++cb) {
       float(&e)[4] = o[i >> 1][2 * cb];

@@ -746,6 +746,85 @@ def test_tree_scales_of_either_sign_that_differ_between_blocks(pa, impl, kv):
     t.check(pa, impl)
 
 
+def within(t, out, lse, rows=None, floor=0.0):
+    """Rows of a step against the oracle under the bounds above, with no slack but ``floor``;
+    infinities and NaN of the outputs where the oracle has values that are not finite."""
+    with np.errstate(all="ignore"):
+        ref, rl, absv, big = t.ref()
+    n = int(t.qs[-1])
+    pick = np.arange(n) if rows is None else np.asarray(rows)
+    o, l = to_f64(out)[pick], to_f64(lse)[pick]
+    ref, rl, absv, big = (x[pick] for x in (ref, rl, absv, big))
+    ctx = np.repeat(t.ctx, t.new)[pick][:, None]
+    dz = 2 * (t.d + 4) * F32 * big
+    fin, fl = np.isfinite(ref), np.isfinite(rl)
+    assert np.array_equal(np.isfinite(o), fin) and np.array_equal(np.isfinite(l), fl)
+    with np.errstate(all="ignore"):
+        E = 2 * (np.expm1(dz) + 2.0 ** -16 + 2.0 ** -21) + ctx * 2.0 ** -23
+        tol = (BF16 + E)[..., None] * absv + BF16 * np.abs(ref) + floor
+        assert (np.abs(o - ref)[fin] <= tol[fin]).all(), float((np.abs(o - ref) / tol)[fin].max())
+        tl = dz + 2.0 ** -15 + ctx * 2.0 ** -23 + 2.0 ** -21 * np.abs(rl)
+        assert (np.abs(l - rl)[fl] <= tl[fl]).all()
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("kv", ["fp8", "int8"])
+@pytest.mark.parametrize("bad", [math.inf, math.nan, 1e30])
+@pytest.mark.parametrize("new", [8, 16, 24, 150])
+def test_tree_scales_of_blocks_that_a_row_does_not_see(pa, impl, kv, bad, new):
+    """A block of drafts with a huge, infinite or NaN scale takes nothing from rows that do not
+    see it, also where it shares a step of keys with context blocks; rows that see it get it."""
+    base = [24, 40, 200]
+    half = new // 2
+    see = [[list(range(i + 1)) if i < half else list(range(0, half // 2)) + list(range(half, i + 1))
+            for i in range(new)] for _ in base]
+    t = Tree(29, base, [new] * 3, 8, 2, 128, 8, kv, see=see)
+    # the block with drafts half .. : the first half's rows see none of it where it begins there
+    at = half // 8 * 8 + (8 if half % 8 else 0)
+    if new == 8:     # one block of drafts: rows 0 to 3 see the context alone
+        at, t.see = 0, [[[] if i < 4 else list(range(i + 1)) for i in range(8)] for _ in base]
+    seen = [[any(at <= j < at + 8 for j in js) for js in s] for s in t.see]
+    for s in range(3):
+        b = t.bt[s, (base[s] + at) // 8]
+        t.o["v_scales"][b] = bad
+        if s == 1 and not math.isinf(bad):
+            t.o["k_scales"][b] = math.nan
+    t.device()
+    out, lse = t.run(pa, impl)
+    assert pa.device_error() == 0
+    seen = np.array([x for s in seen for x in s])
+    assert seen.any() and not seen.all()
+    within(t, out, lse, np.flatnonzero(~seen))
+    assert np.isfinite(to_f64(out)[:len(seen)][~seen]).all()
+    if not math.isnan(bad):
+        finite = math.isfinite(bad)
+        keep = [i for i in np.flatnonzero(seen) if i // new != 1]
+        if finite:
+            # A weight times its V scale is held in f16 relative to a power of two of at most twice
+            # the largest scale, times 2^7: to half a step of 2^-24, or 2^-31 of that scale. Where
+            # the huge block's codes are 0 this is what is left of the others' |code| <= 448 (the
+            # sum of weights that divides them is at least 1).
+            within(t, out, lse, keep, floor=float(t.ctx.max()) * 448 * 2.0 ** -31 * bad)
+        else:
+            assert not np.isfinite(to_f64(out)[keep]).any()
+    else:
+        assert np.isnan(to_f64(out)[:len(seen)][seen]).all()
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("kv", ["fp8", "int8"])
+@pytest.mark.parametrize("e", [-100, 114])
+def test_tree_scales_near_the_ends_of_float32(pa, impl, kv, e):
+    """V scales about 2^(e - 7): weights that carry them stay within the format they are rounded to
+    (and, with a few hundred tokens, sums of values of 2^(e + 2) within float32)."""
+    t = Tree(30, [300, 3], [6, 40], 8, 2, 128, 16, kv)
+    t.o["v_scales"] *= np.float32(2.0 ** e)
+    t.device()
+    out, lse = t.run(pa, impl)
+    assert pa.device_error() == 0
+    within(t, out, lse)
+
+
 def test_tree_two_calls_at_once_and_other_streams(pa):
     """Calls on two streams with a workspace each, and on a side stream, give the same results."""
     a, b = Tree(16, [3000, 40], [8, 5], 8, 2, 128, 16, "bf16"), Tree(17, [700] * 9, [4] * 9, 8, 2, 128, 16, "fp8")
