@@ -26,10 +26,11 @@
 //
 // Types: a bf16 cache is multiplied as it is, with P rounded to bf16. Codes of one byte become
 // f16 in registers: E4M3 values and code - zero are exact. Q rows are brought to [2^14, 2^15) by
-// a power of two each, which bf16's eight bits survive down to 2^-28 of the row's largest
-// element. P carries V scale / v_ref * 2^7, v_ref a power of two, for each row no smaller than any
-// |V scale| of the keys that it has seen: at most 2^15, and f16 holds it to 11 bits down to 2^-21
-// of the largest. Scales of keys that a row does not see, infinite ones too, do not reach it.
+// a power of two each (2^126 at most: short of that for rows below 2^-112), and bf16's eight bits
+// survive that down to 2^-28 of the row's largest element. P carries V scale / v_ref * 2^7, v_ref
+// a power of two, for each row no smaller than any |V scale| of the keys that it has seen: at most
+// 2^15, and f16 holds it to 11 bits down to 2^-21 of the largest. Scales of keys that a row does
+// not see, infinite ones too, do not reach it.
 #pragma once
 
 #include "decode_tc.cuh"
@@ -238,7 +239,8 @@ tree_mma_kernel(const TreeArgs a, int rts) {
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const int eb = (int)((__float_as_uint(amax) >> 23) & 0xff);
-      const int e = eb == 0 || eb == 0xff ? 0 : max(-100, min(100, 14 - (eb - 127)));
+      // -113 for the largest bf16; both 2^e and 2^-e stay normal, so rows of subnormals stop at 126
+      const int e = amax == 0.f || eb == 0xff ? 0 : min(126, 14 - (eb - 127));
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);

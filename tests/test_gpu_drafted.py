@@ -825,6 +825,23 @@ def test_tree_scales_near_the_ends_of_float32(pa, impl, kv, e):
     within(t, out, lse)
 
 
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("kv,e", [("bf16", 116), ("bf16", -100)] +
+                         [(kv, e) for kv in ("fp8", "int8") for e in (118, 124, -100, -124)])
+@pytest.mark.parametrize("new", [3, 33])
+def test_tree_query_rows_of_any_size(pa, impl, kv, e, new):
+    """Query rows near both ends of bf16's range, with a scale that brings their scores back (for a
+    bf16 cache as far as sums of 128 products stay within float32); every other row is small."""
+    t = Tree(31, [70, 300], [new, 2], 8, 2, 128, 16, kv)
+    t.q[::2] *= 2.0 ** e
+    t.scale *= 2.0 ** -e
+    if e < 0:
+        t.q[1::2] *= 2.0 ** (e - 2)
+    out, lse = t.run(pa, impl)
+    assert pa.device_error() == 0
+    within(t, out, lse)
+
+
 def test_tree_two_calls_at_once_and_other_streams(pa):
     """Calls on two streams with a workspace each, and on a side stream, give the same results."""
     a, b = Tree(16, [3000, 40], [8, 5], 8, 2, 128, 16, "bf16"), Tree(17, [700] * 9, [4] * 9, 8, 2, 128, 16, "fp8")
