@@ -4,6 +4,8 @@
 // A drafted step makes half a dozen calls of a few microseconds each, with up to fifteen
 // tensors. Asking each tensor through its Python methods costs about 0.4 us, more in all than
 // the launches; reading the tensor objects directly costs a few nanoseconds.
+#include <exception>
+
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -20,6 +22,25 @@ void refuse(PyObject* t, PyObject* name, PyObject* dtype, PyObject* dev, PyObjec
   if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a tensor does not fit the call");
 }
 
+// Tensors of some kinds throw where their memory or sizes are asked for (batched by a transform,
+// nested, sparse): f's exceptions become Python's, none may reach the interpreter's C frames.
+template <typename F>
+PyObject* guarded(F f) {
+  try {
+    return f();
+  } catch (python_error& e) {
+    e.restore();
+  } catch (const c10::Error& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+  } catch (const std::exception& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+  }
+  if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "a tensor could not be read");
+  return nullptr;
+}
+
+// A shape's entry that is no integer leaves a Python error behind.
 bool same_shape(const at::Tensor& t, PyObject* shape) {
   if (shape == Py_None) return true;
   if (!PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) != t.dim()) return false;
@@ -56,11 +77,13 @@ PyObject* ptrs(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (a[0] == Py_None) {
       p = Py_NewRef(Py_None);
     } else {
-      const at::Tensor* t = tensor_on(a[0], a[2], dev);
-      if (t != nullptr && t->is_contiguous() && same_shape(*t, a[3]))
-        p = PyLong_FromVoidPtr(t->data_ptr());
-      else
-        refuse(a[0], a[1], a[2], args[0], a[3]);
+      p = guarded([&]() -> PyObject* {
+        const at::Tensor* t = tensor_on(a[0], a[2], dev);
+        if (t != nullptr && t->is_contiguous() && same_shape(*t, a[3]))
+          return PyLong_FromVoidPtr(t->data_ptr());
+        if (!PyErr_Occurred()) refuse(a[0], a[1], a[2], args[0], a[3]);
+        return nullptr;
+      });
       if (p == nullptr) {
         Py_DECREF(out);
         return nullptr;
@@ -80,15 +103,17 @@ PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   const long dev = PyLong_AsLong(args[0]);
   if (dev == -1 && PyErr_Occurred()) return nullptr;
-  const at::Tensor* t = tensor_on(args[1], args[3], dev);
-  if (t == nullptr || t->dim() != 3 || !same_shape(*t, args[4]) ||
-      (t->stride(2) != 1 && t->size(2) > 1) || (t->stride(1) != t->size(2) && t->size(1) > 1)) {
-    refuse(args[1], args[2], args[3], args[0], args[4]);
-    return nullptr;
-  }
-  // a single row has no stride of its own
-  const int64_t stride = t->size(0) > 1 ? t->stride(0) : t->size(1) * t->size(2);
-  return Py_BuildValue("NL", PyLong_FromVoidPtr(t->data_ptr()), (long long)stride);
+  return guarded([&]() -> PyObject* {
+    const at::Tensor* t = tensor_on(args[1], args[3], dev);
+    if (t == nullptr || t->dim() != 3 || !same_shape(*t, args[4]) ||
+        (t->stride(2) != 1 && t->size(2) > 1) || (t->stride(1) != t->size(2) && t->size(1) > 1)) {
+      if (!PyErr_Occurred()) refuse(args[1], args[2], args[3], args[0], args[4]);
+      return nullptr;
+    }
+    // a single row has no stride of its own
+    const int64_t stride = t->size(0) > 1 ? t->stride(0) : t->size(1) * t->size(2);
+    return Py_BuildValue("NL", PyLong_FromVoidPtr(t->data_ptr()), (long long)stride);
+  });
 }
 
 PyObject* on_refusal(PyObject*, PyObject* f) {

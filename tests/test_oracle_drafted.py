@@ -2,6 +2,9 @@
 trees and closed forms; and refusals of the library's entry points that need no device."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -314,3 +317,41 @@ def test_binding_refuses_host_tensors(pa):
                        next_tokens=torch.zeros(1, dtype=torch.int64), kept_lens=i(1))
     with pytest.raises(ValueError):
         pa.compact_accepted(b(4, 2, 16, 64), b(4, 2, 16, 64), i(1, 3), i(1), i(2), i(1, 4), i(1))
+
+
+UNREADABLE = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+import paged_kv_cache_465_b200 as pa
+
+def i(*n): return torch.empty(*n, dtype=torch.int32, device="cuda")
+def l(*n): return torch.empty(*n, dtype=torch.int64, device="cuda")
+def b(*n): return torch.empty(*n, dtype=torch.bfloat16, device="cuda")
+
+def verify(parents):
+    pa.tree_verify(parents, l(4), l(4), i(2), i(1), accepted=i(1, 2), num_accepted=i(1),
+                   next_tokens=l(1), kept_lens=i(1))
+    return parents
+
+def rotary(q):
+    pa.rotary_and_cache(q, b(2, 2, 64), b(2, 2, 64), b(2, 4, 64), b(4, 2, 16, 64), b(4, 2, 16, 64),
+                        i(2), l(2), torch.ones(32, device="cuda"))
+    return q
+
+with FakeTensorMode():
+    for f, x in ((verify, i(3, 4)), (rotary, b(3, 2, 4, 64))):
+        try:
+            torch.func.vmap(f)(x)
+        except RuntimeError as e:
+            print("raised:", str(e).splitlines()[0])
+"""
+
+
+def test_tensors_without_readable_memory_raise(pa):
+    """A tensor that a transform has batched has no pointer: an error, as any other, not the end of
+    the process."""
+    r = subprocess.run([sys.executable, "-W", "ignore", "-c", UNREADABLE], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
+    said = [line for line in r.stdout.splitlines() if line.startswith("raised:")]
+    assert len(said) == 2 and all("storage" in line for line in said), r.stdout
