@@ -18,9 +18,9 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedattn.so")
 
-if not os.path.exists(LIB_PATH) or not os.path.exists(os.path.join(_HERE, "_tensors.so")):
+if not os.path.exists(LIB_PATH):
     raise ImportError(
-        f"{LIB_PATH} or _tensors.so beside it is missing: build them with `python paged_kv_cache_465_b200/build.py` "
+        f"{LIB_PATH} is missing: build it with `python paged_kv_cache_465_b200/build.py` "
         "(nvcc, sm_100a). There is no non-CUDA implementation.")
 
 _lib = ctypes.CDLL(LIB_PATH)

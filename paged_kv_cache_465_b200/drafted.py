@@ -7,8 +7,11 @@ stays on the GPU: no call synchronises, so a step can be captured in a CUDA grap
 """
 from __future__ import annotations
 
+import importlib.util
+import os
 from typing import Optional, Sequence
 
+from .build import helper_path
 from . import (PARTITION_AUTO, PA_ERR_WORKSPACE, PA_OK, PagedAttnError, _dtype_code, _lib, _torch,
                pa_decode_desc, pa_rotary_desc)
 
@@ -43,10 +46,16 @@ def _rows(*args):
 
 def _load_helper() -> None:
     global _ptrs, _rows
-    _torch()
-    from . import _tensors
-    _tensors.on_refusal(_refuse)
-    _ptrs, _rows = _tensors.ptrs, _tensors.rows
+    path = helper_path(_torch())
+    if not os.path.exists(path):
+        raise ImportError(
+            f"{path}, the checks of tensors for this torch and Python, is missing: build it with "
+            "`python paged_kv_cache_465_b200/build.py`")
+    spec = importlib.util.spec_from_file_location(__package__ + "._tensors", path)
+    helper = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(helper)
+    helper.on_refusal(_refuse)
+    _ptrs, _rows = helper.ptrs, helper.rows
 
 
 def _launch(fn, what: str, dev: int, stream, args) -> None:
