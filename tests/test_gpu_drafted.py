@@ -746,9 +746,10 @@ def test_tree_scales_of_either_sign_that_differ_between_blocks(pa, impl, kv):
     t.check(pa, impl)
 
 
-def within(t, out, lse, rows=None, floor=0.0):
-    """Rows of a step against the oracle under the bounds above, with no slack but ``floor``;
-    infinities and NaN of the outputs where the oracle has values that are not finite."""
+def within(t, out, lse, rows=None, floor=0.0, weight=BF16):
+    """Rows of a step against the oracle under the bounds above, with no slack but ``floor`` and
+    weights rounded by ``weight``; infinities and NaN of the outputs where the oracle has values
+    that are not finite."""
     with np.errstate(all="ignore"):
         ref, rl, absv, big = t.ref()
     n = int(t.qs[-1])
@@ -761,7 +762,7 @@ def within(t, out, lse, rows=None, floor=0.0):
     assert np.array_equal(np.isfinite(o), fin) and np.array_equal(np.isfinite(l), fl)
     with np.errstate(all="ignore"):
         E = 2 * (np.expm1(dz) + 2.0 ** -16 + 2.0 ** -21) + ctx * 2.0 ** -23
-        tol = (BF16 + E)[..., None] * absv + BF16 * np.abs(ref) + floor
+        tol = (weight + E)[..., None] * absv + BF16 * np.abs(ref) + floor
         assert (np.abs(o - ref)[fin] <= tol[fin]).all(), float((np.abs(o - ref) / tol)[fin].max())
         tl = dz + 2.0 ** -15 + ctx * 2.0 ** -23 + 2.0 ** -21 * np.abs(rl)
         assert (np.abs(l - rl)[fl] <= tl[fl]).all()
@@ -823,6 +824,20 @@ def test_tree_scales_near_the_ends_of_float32(pa, impl, kv, e):
     out, lse = t.run(pa, impl)
     assert pa.device_error() == 0
     within(t, out, lse)
+
+
+@pytest.mark.parametrize("kv", ["fp8", "int8"])
+@pytest.mark.parametrize("new", [8, 40])
+def test_tree_weights_over_codes_are_f16(pa, kv, new):
+    """Over one-byte codes a weight times its V scale is held in f16: to 2^-11 of itself, or half a
+    step of 2^-24 relative to 2^-7 v_ref, v_ref at most twice the largest V scale (2^-31 of it for
+    a code of 1; codes reach 448). The sum of the weights that divides them is at least 1. In
+    channels that cancel, bf16 weights would pass the bound."""
+    t = Tree(33, [2, 5, 40, 300], [new] * 4, 8, 2, 128, 16, kv)
+    out, lse = t.run(pa)
+    assert pa.device_error() == 0
+    top = float(np.abs(t.o["v_scales"]).max())
+    within(t, out, lse, floor=float(t.ctx.max()) * 448 * 2.0 ** -31 * top, weight=2.0 ** -11)
 
 
 @pytest.mark.parametrize("impl", IMPLS)
