@@ -453,18 +453,20 @@ tree_mma_kernel(const TreeArgs a, int rts) {
             vs[nt] = s_vs[b];
             vmax = fmaxf(vmax, fabsf(vs[nt]));
           }
-          bool up = false;
+          bool up = vmax > vref[0];   // unmasked: of all rows
 #pragma unroll
-          for (int i = 0; i < MT * 2; ++i) {
-            seen[i] = vmax;
-            if (masked) {
+          for (int i = 0; i < MT * 2; ++i) seen[i] = vmax;
+          if (masked) {
+            up = false;
+#pragma unroll
+            for (int i = 0; i < MT * 2; ++i) {
               const uint32_t v = (uint32_t)(view[i] >> k0);
               seen[i] = 0.f;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 if ((v >> (8 * nt)) & 0xffu) seen[i] = fmaxf(seen[i], fabsf(vs[nt]));
+              up = up || seen[i] > vref[i];
             }
-            up = up || seen[i] > vref[i];
           }
           if (__any_sync(0xffffffffu, up)) {
             // The next power of two, within a range in which 2^7 over it is one too; what was
