@@ -425,6 +425,11 @@ size_t paged_attn_tree_workspace_size(const pa_decode_desc* desc, int num_tokens
  * group of 1, 2, 4, 8 or 16 run on the tensor cores; other shapes, or
  * pa_set_decode_impl(1), on the CUDA cores. Rows behind query_start[num_seqs] are neither
  * read nor written. Results depend on lengths and values, not on where blocks sit.
+ * Precision: sums, softmax statistics and the joining of parts are float32 everywhere. The
+ * tensor cores multiply V by weights rounded to bf16 for a bf16 cache (2^-8 relative), to f16
+ * for one-byte caches (2^-11); the CUDA cores round nothing but the output.
+ * max_context_len also sets how contexts are cut over the GPU: a limit far above the lengths
+ * in the batch gives the same results, later.
  */
 pa_status paged_attn_tree(const void* q, const void* k_cache, const void* v_cache,
                           const int32_t* block_tables, const int32_t* context_lens,

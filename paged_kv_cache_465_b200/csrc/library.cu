@@ -47,12 +47,17 @@ int tree_simt_parts(const pa_decode_desc* d, int num_tokens, int max_context_len
 bool tree_mma(const pa_decode_desc* d) { return prefill_tc_supported(d); }
 
 // Tokens of a part on the tensor cores. Few (row tile, sequence, kv head)s: as many parts as make
-// just under 1776 CTAs, two or three rounds for each place on the SMs, when the lengths are alike
-// (8 x 65536 tokens: 27 parts 372 us, 28 parts, which make a round of a few CTAs, 395; 64 parts
-// 456). Many: they fill the places by themselves, and only a context much longer than others is
-// cut, for the last round's sake (256 of 16 .. 8192 tokens: 2048-token parts 246 us, 4096 260; 256
-// of 1024: whole 212 us, halves 283). Parts under 128 tokens cost more to join than they give.
-// The parts' results stay within 192 MB (a thousandth of the GPU's memory): longer parts otherwise.
+// just under 1776 CTAs when every context is as long as allowed, four rounds of the 444 places that
+// tiles of 32 and 64 rows have, six of 296 with 128 rows (8 x 65536 bf16 tokens: 27 parts 352 us;
+// 28, which begin a fifth round of a few CTAs, 380; 61 parts 415, 17 parts 397). Many: parts of 2048
+// tokens, so that the longest contexts do not make the last round alone (256 of 16 .. 8192 fp8
+// tokens: 215 us; 4096-token parts 227, 1024 229, whole contexts 251). Contexts of one length pay
+// for that cut: 256 of 2056 fp8 tokens, cut into 2048 and 8, take 364 us and 297 whole (256 of 1032,
+// left whole, 173, and 228 in halves). Parts under 128 tokens cost more to join than they give. The
+// parts' results stay within 192 MB (a thousandth of the GPU's memory): longer parts otherwise.
+// The rule knows what is allowed, not the lengths, which are on the device: with 131072 allowed,
+// 32 requests of at most 4112 bf16 tokens take 113 us instead of 45, 256 of at most 8200 fp8 tokens
+// 265 instead of 215, 13 of at most 20064 int8 tokens 413 instead of 113.
 int tree_mma_part(const pa_decode_desc* d, int num_tokens, int max_query_len,
                   int max_context_len) {
   const int group = d->num_q_heads / d->num_kv_heads, R = tree::mma_rows(max_query_len, group);

@@ -9,7 +9,7 @@
 //
 // Bound: HBM. Per token it reads q, k, v once and writes q_out and the two cache rows once;
 // the unfused sequence would write k and read it again. Loads are issued before the angles
-// are formed. A step's few tokens are bound by latency instead (3 us).
+// are formed. A step's few tokens are bound by latency instead (4 us).
 #pragma once
 
 #include "common.cuh"

@@ -10,19 +10,20 @@
 // Work split: one CTA of four warps per (part of the context, row tile, kv head, sequence). 32 rows
 // split over two pairs of warps (16 rows each), a pair taking half of a tile's keys, and the pairs
 // join at the end; 64 rows are 16 to a warp. 16 rows keep a warp within 168 registers with Q in
-// them, and three CTAs on an SM, which hides each other's waits: against two CTAs of 32 rows to a
-// warp, 256 sequences of 1024 fp8 tokens took 176 us instead of 212 and 8 x 65536 bf16 tokens 352
-// instead of 398. 128 rows do take 32 to a warp, a fragment of K or V then feeding two products
+// them, and three CTAs on an SM, which hides each other's waits: 256 sequences of 1024 fp8 tokens
+// take 173 us (212 with two CTAs of 32 rows to a warp) and 8 x 65536 bf16 tokens 352 (398). 128 rows do take 32 to a warp, a fragment of K or V then feeding two products
 // (1560 us for 8 x 131072 tokens with 128 rows; two 64-row tiles, the second reading K and V from
 // L2, 1741).
 // Keys pass through a ring of shared-memory stages that asynchronous copies fill; zero for what is
 // not there, so that no product reads undefined memory. There are no flags or barriers in memory
 // and no waits but the CTA's own.
 //
-// Bound: HBM for a bf16 cache and up to 32 rows (8 x 65536 tokens: 352 us, 93 % of the measured
-// copy rate). Beyond, and for codes, the latency of the chain fragment - product - softmax - product
-// in the few warps that registers leave: the tensor pipe is busy 33 - 38 % of the time, the issue
-// slots 30 - 40 %, and HBM gets to 47 % (8 x 65536 fp8 tokens 312 us).
+// Bound: HBM for a bf16 cache and up to 32 rows of long contexts (8 x 65536 tokens: 352 us, 93 % of
+// the measured copy rate). Beyond, and for codes, the latency of the chain fragment - product -
+// softmax - product in the few warps that registers leave: with 128 rows the tensor pipe is busy
+// 49 % of the time and the issue slots 32 % (HBM 42 % at 8 x 131072 tokens, 1560 us); for fp8 with 32
+// rows tensor 40 %, alu 46 %, issue 52 % (each code becomes f16 in every warp whose rows need it; HBM
+// 52 % at 8 x 65536 tokens, 314 us). Ragged batches are bound by the longest part (library.cu).
 //
 // Types: a bf16 cache is multiplied as it is, with P rounded to bf16. Codes of one byte become
 // f16 in registers: E4M3 values and code - zero are exact. Q rows are brought to [2^14, 2^15) by

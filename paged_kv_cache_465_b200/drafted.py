@@ -115,7 +115,8 @@ def build_step(context_lens, new_lens, blocks_held, block_tables, free_blocks, q
     [rows, words] (bit j % 32 of word j / 32: the row sees row j of its sequence), status [1]
     (0, or the PA_DEVERR_* bits for which the step was refused as a whole). block_tables gets
     the new entries. ``parents`` [rows]: index within the sequence of each row's parent, -1
-    for none; without it rows form a chain.
+    for none; without it rows form a chain. With no sequences (S = 0) every output is
+    written too: no rows, no slots, the queue passed on.
     """
     torch = _torch()
     i32, dev = torch.int32, _device(context_lens, "context_lens")
